@@ -1,0 +1,78 @@
+// Internal view of the paged 8-bit cache (include/moba.h) and the launchers
+// of its kernels.  As in launch.h, every launcher enqueues on `st` and
+// returns the launch status; none allocates or synchronises.
+#pragma once
+
+#include "common.cuh"
+
+namespace moba {
+namespace cache {
+
+typedef __nv_bfloat16 bf16;
+
+enum : int32_t {
+  kStatusNoPages = 1 << 4,    // a row was refused
+  kStatusBadTable = 1 << 5,   // row state, page number or plan entry out of range; skipped
+  kStatusNonFinite = 1 << 6   // a NaN or infinity was stored as 0
+};
+
+constexpr int kHistRing = 16;  // raw keys kept per row for the key conv
+constexpr int kMaxWidth = 8;
+
+// Device pointers and sizes of a cache; kernels take it by value.
+struct View {
+  int rows, n_pages, max_blocks, h_kv, d, B, kind, conv_width;
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  bf16* cent;
+  bf16* tail_k;
+  bf16* tail_v;
+  bf16* hist;
+  int32_t* table;
+  int32_t* state;
+  int32_t* free_pages;
+  long long* ring;
+};
+
+struct Plan {
+  int T;
+  int32_t* cu;
+  int32_t* row;
+  int32_t* pos;
+  int32_t* slot;
+};
+
+// What kernel one of moba_cache_tables leaves for kernel two, per row.
+struct RowPlan {
+  int32_t length;  // tokens before the step
+  int32_t held;    // pages before the step
+  int32_t from;    // ring index of the first page taken (releasing rows: of the first page given back)
+  int32_t flags;   // kRowServed, kRowRelease
+};
+constexpr int kRowServed = 1, kRowRelease = 2;
+
+cudaError_t launch_reset(const View& c, cudaStream_t st);
+cudaError_t launch_tables(const View& c, const int32_t* new_len, int32_t* state_out, long long* ring_out,
+                          const Plan& p, RowPlan* rp, int32_t* status, cudaStream_t st);
+cudaError_t launch_append(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* conv_w,
+                          int32_t* status, cudaStream_t st);
+// Workspace of the router and of attention beyond the status word, in bytes.
+size_t route_scratch(const View& c, int T, int h_q);
+cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, int topk, int32_t* sel, void* scratch,
+                         int32_t* status, cudaStream_t st);
+size_t attn_scratch(const View& c, int T, int h_q);
+cudaError_t launch_attention(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk,
+                             bf16* out, float* lse, void* scratch, int32_t* status, cudaStream_t st);
+
+// Where block j of a row is read from: its page (complete blocks), its tail
+// bank, or nowhere (an entry out of range).
+__device__ __forceinline__ int block_page(const View& c, int row, int j) {
+  if (j < 0 || j >= c.max_blocks) return -1;
+  const int pg = __ldg(c.table + (size_t)row * c.max_blocks + j);
+  return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
+}
+
+}  // namespace cache
+}  // namespace moba

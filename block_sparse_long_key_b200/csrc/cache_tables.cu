@@ -1,0 +1,212 @@
+// Block tables and slot maps of the paged cache, built on the device from the
+// rows' lengths, so that no step waits for the host.
+//
+// Row r with L tokens in `held` pages, getting n more, needs
+//   need_r = max(0, ceil((L + n) / B) - held)
+// pages.  They come from a FIFO ring of free pages in row order, so row r's
+// are ring entries [head + S_r - need_r, head + S_r) with S the inclusive sum
+// of need: a scan.  Row r is served iff S_r <= free pages.  Pages of finished
+// rows go behind the ring's end and can be taken from the next step on, so
+// what is taken and what is given back never meet.
+//
+// Kernel one scans the rows in one CTA and writes the state after the step
+// (it is the only one to read the state before, so both may be one buffer);
+// kernel two lists the tokens, one thread per token.  A page is first used by
+// the token at its start (pages are taken only for blocks without tokens), so
+// that token's thread writes the block table entry.
+#include "cache.cuh"
+
+namespace moba {
+namespace cache {
+namespace {
+
+constexpr int kScanThreads = 1024;
+constexpr int kFillThreads = 256;
+
+struct Sums {
+  long long tokens, need, gone;
+};
+
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return Sums{a.tokens + b.tokens, a.need + b.need, a.gone + b.gone};
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums& s, int off) {
+  return Sums{__shfl_up_sync(~0u, s.tokens, off), __shfl_up_sync(~0u, s.need, off), __shfl_up_sync(~0u, s.gone, off)};
+}
+
+// Inclusive scan over the CTA.
+__device__ Sums block_scan(Sums s, Sums* warp_sums) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int off = 1; off < 32; off <<= 1) {
+    const Sums o = shfl_up(s, off);
+    if (lane >= off) s = s + o;
+  }
+  if (lane == 31) warp_sums[w] = s;
+  __syncthreads();
+  if (w == 0) {
+    Sums t = lane < nw ? warp_sums[lane] : Sums{0, 0, 0};
+    for (int off = 1; off < 32; off <<= 1) {
+      const Sums o = shfl_up(t, off);
+      if (lane >= off) t = t + o;
+    }
+    if (lane < nw) warp_sums[lane] = t;
+  }
+  __syncthreads();
+  return w ? s + warp_sums[w - 1] : s;
+}
+
+__global__ void __launch_bounds__(kScanThreads)
+scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_out, Plan p, RowPlan* rp,
+            int32_t* status) {
+  __shared__ Sums warp_sums[32];
+  __shared__ Sums carry;
+  __shared__ long long taken;
+  const int tid = threadIdx.x;
+  long long head = c.ring[0], tail = c.ring[1];
+  const bool ring_ok = head >= 0 && tail >= head && tail - head <= c.n_pages;
+  if (!ring_ok) head = tail = 0;
+  const long long avail = tail - head;
+  if (tid == 0) {
+    status[0] = ring_ok ? 0 : kStatusBadTable;
+    status[1] = 0;
+    carry = Sums{0, 0, 0};
+    taken = 0;
+    p.cu[0] = 0;
+  }
+  __syncthreads();
+  for (int base = 0; base < c.rows; base += kScanThreads) {
+    const int r = base + tid;
+    int L = 0, held = 0, n = 0;
+    bool ok = true;
+    long long total = 0;
+    Sums s{0, 0, 0};
+    if (r < c.rows) {
+      L = c.state[2 * r], held = c.state[2 * r + 1], n = new_len[r];
+      if (L < 0 || held < 0 || held > c.max_blocks || L > (long long)held * c.B) {
+        set_status(status, kStatusBadTable);
+        ok = false;
+        L = held = 0;
+      }
+      total = ((long long)L + max(n, 0) + c.B - 1) / c.B;
+      if (total > c.max_blocks) {
+        set_status(status, kStatusNoPages);
+        ok = false;
+      }
+      s.tokens = max(n, 0);
+      if (ok && n >= 0) s.need = max(total - held, 0ll);
+      if (n < 0) s.gone = held;
+    }
+    const Sums mine = s;
+    s = block_scan(s, warp_sums) + carry;
+    if (r < c.rows) {
+      if (mine.need > 0 && s.need > avail) {
+        set_status(status, kStatusNoPages);
+        ok = false;
+      }
+      if (s.tokens > p.T) {
+        if (n > 0) ok = false;
+        set_status(status, kStatusBadSeqlens);
+      }
+      RowPlan q;
+      q.length = L, q.held = held;
+      q.flags = n < 0 ? kRowRelease : (ok ? kRowServed : 0);
+      const long long from = n < 0 ? tail + s.gone - mine.gone : head + s.need - mine.need;
+      q.from = (int)(from % c.n_pages);
+      rp[r] = q;
+      p.cu[r + 1] = (int)(s.tokens < p.T ? s.tokens : p.T);
+      if (n < 0) {
+        state_out[2 * r] = 0, state_out[2 * r + 1] = 0;
+      } else if (ok) {
+        state_out[2 * r] = L + n, state_out[2 * r + 1] = held + (int)mine.need;
+        if (mine.need) atomicAdd(reinterpret_cast<unsigned long long*>(&taken), (unsigned long long)mine.need);
+      } else {
+        state_out[2 * r] = c.state[2 * r], state_out[2 * r + 1] = c.state[2 * r + 1];
+      }
+    }
+    __syncthreads();
+    if (tid == kScanThreads - 1) carry = s;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    if (carry.gone > c.n_pages - avail) atomicOr(status, kStatusBadTable);
+    ring_out[0] = head + taken;
+    ring_out[1] = tail + carry.gone;
+  }
+}
+
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(View c, Plan p, const RowPlan* rp, int32_t* status) {
+  const int nth = gridDim.x * kFillThreads;
+  const int total = __ldg(p.cu + c.rows);
+  for (long long i = blockIdx.x * kFillThreads + threadIdx.x; i < p.T; i += nth) {
+    const int t = (int)i;
+    int row = -1, pos = -1, slot = -1;
+    if (t < total) {
+      row = upper_seq(p.cu, c.rows, t);
+      const RowPlan q = rp[row];
+      if (q.flags & kRowServed) {
+        pos = q.length + t - __ldg(p.cu + row);
+        const int j = pos / c.B;
+        int32_t* entry = c.table + (size_t)row * c.max_blocks + j;
+        int pg;
+        if (j < q.held) {
+          pg = *entry;
+        } else {
+          pg = c.free_pages[((long long)q.from + j - q.held) % c.n_pages];
+          if (pos % c.B == 0) *entry = pg;
+        }
+        if ((unsigned)pg < (unsigned)c.n_pages) slot = pg * c.B + pos % c.B;
+        else set_status(status, kStatusBadTable);
+      }
+    }
+    p.row[t] = row, p.pos[t] = pos, p.slot[t] = slot;
+  }
+  for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
+    const RowPlan q = rp[r];
+    if (!(q.flags & kRowRelease)) continue;
+    for (int i = threadIdx.x; i < q.held; i += kFillThreads)
+      c.free_pages[((long long)q.from + i) % c.n_pages] = c.table[(size_t)r * c.max_blocks + i];
+  }
+}
+
+__global__ void __launch_bounds__(kFillThreads) reset_kernel(View c) {
+  const size_t nth = (size_t)gridDim.x * kFillThreads;
+  const size_t i0 = (size_t)blockIdx.x * kFillThreads + threadIdx.x;
+  for (size_t i = i0; i < (size_t)c.n_pages; i += nth) c.free_pages[i] = (int)i;
+  for (size_t i = i0; i < (size_t)c.rows * c.max_blocks; i += nth) c.table[i] = -1;
+  for (size_t i = i0; i < (size_t)c.rows * 2; i += nth) c.state[i] = 0;
+  const size_t tail = (size_t)c.rows * 2 * c.h_kv * c.B * c.d / 8;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  for (size_t i = i0; i < tail; i += nth) {
+    reinterpret_cast<uint4*>(c.tail_k)[i] = z;
+    reinterpret_cast<uint4*>(c.tail_v)[i] = z;
+  }
+  if (c.conv_width > 1)
+    for (size_t i = i0; i < (size_t)c.rows * kHistRing * c.h_kv * c.d / 8; i += nth)
+      reinterpret_cast<uint4*>(c.hist)[i] = z;
+  if (i0 == 0) {
+    c.ring[0] = 0;
+    c.ring[1] = c.n_pages;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_reset(const View& c, cudaStream_t st) {
+  reset_kernel<<<592, kFillThreads, 0, st>>>(c);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tables(const View& c, const int32_t* new_len, int32_t* state_out, long long* ring_out,
+                          const Plan& p, RowPlan* rp, int32_t* status, cudaStream_t st) {
+  scan_kernel<<<1, kScanThreads, 0, st>>>(c, new_len, state_out, ring_out, p, rp, status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int work = p.T > c.rows ? p.T : c.rows;
+  const int grid = (work + kFillThreads - 1) / kFillThreads;
+  fill_kernel<<<grid < 1184 ? grid : 1184, kFillThreads, 0, st>>>(c, p, rp, status);
+  return cudaGetLastError();
+}
+
+}  // namespace cache
+}  // namespace moba

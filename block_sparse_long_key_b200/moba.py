@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -20,6 +20,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "moba.h")
 
 MOBA_OK, MOBA_EINVAL, MOBA_EALIGN, MOBA_EWORKSPACE, MOBA_ELAUNCH, MOBA_EDEVICE = 0, -1, -2, -3, -4, -5
 STATUS_BAD_SEQLENS, STATUS_BAD_SEL_IDX, STATUS_INDEX_OVERFLOW, STATUS_TIMEOUT = 1, 2, 4, 8
+STATUS_NO_PAGES, STATUS_BAD_TABLE, STATUS_NONFINITE = 16, 32, 64
 PATH_ROUTE_TCGEN05, PATH_FWD_TCGEN05, PATH_BWD_TCGEN05, PATH_EXACT_ROWS = 1, 2, 4, 8
 
 
@@ -33,6 +34,18 @@ class Shape(ctypes.Structure):
         ("block_size", ctypes.c_int32),
         ("topk", ctypes.c_int32),
     ]
+
+
+class CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n_pages", "max_blocks", "h_kv", "head_dim", "block_size", "kind",
+                                              "conv_width")] + \
+               [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "cent", "tail_k", "tail_v", "hist",
+                                               "block_table", "row_state", "free_pages", "ring")]
+
+
+class PlanStruct(ctypes.Structure):
+    _fields_ = [("total_new", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("cu_new", "token_row", "token_pos", "slot_map")]
 
 
 class MobaError(RuntimeError):
@@ -76,6 +89,19 @@ def lib() -> ctypes.CDLL:
         L.moba_check_path.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.moba_check_path.restype = I
         L.moba_status_string.argtypes = [I]
+        C, N = ctypes.POINTER(CacheStruct), ctypes.POINTER(PlanStruct)
+        L.moba_cache_workspace_size.argtypes = [C, I, I]
+        L.moba_cache_workspace_size.restype = S
+        L.moba_cache_reset.argtypes = [C, P]
+        L.moba_cache_reset.restype = I
+        L.moba_cache_tables.argtypes = [C, P, P, P, N, P, S, P]
+        L.moba_cache_tables.restype = I
+        L.moba_cache_append.argtypes = [C, N, P, P, P, P, S, P]
+        L.moba_cache_append.restype = I
+        L.moba_cache_route.argtypes = [C, N, P, I, I, P, P, S, P]
+        L.moba_cache_route.restype = I
+        L.moba_cache_attention.argtypes = [C, N, P, I, P, I, P, P, P, S, P]
+        L.moba_cache_attention.restype = I
         L.moba_status_string.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -292,3 +318,233 @@ def selftest_bounded_wait(limit_ns: int, workspace: torch.Tensor) -> None:
     on the current stream; read the outcome with ``check_status``."""
     _check(lib().moba_selftest_bounded_wait(int(limit_ns), _ptr(workspace), workspace.numel(), _stream()),
            "moba_selftest_bounded_wait")
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+CACHE_KINDS = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
+_CACHE_HIST = 16
+
+
+class CachePlan(NamedTuple):
+    """The new tokens of a step (see moba_cache_plan), packed row after row."""
+    cu_new: torch.Tensor     # int32 [rows + 1]
+    token_row: torch.Tensor  # int32 [T]
+    token_pos: torch.Tensor  # int32 [T]
+    slot_map: torch.Tensor   # int32 [T]
+
+
+class Cache:
+    """The buffers of a paged 8-bit cache (layouts: moba_cache in include/moba.h), checked once.
+
+    ``alloc_cache`` makes an empty one.  Built from tensors of the caller, those
+    that a call does not use may be None (bookkeeping alone needs block_table,
+    row_state, free_pages and ring).  The tensors are fixed: write into them,
+    do not rebind them."""
+
+    def __init__(self, *, rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: int, block_size: int,
+                 kind: str = "e4m3", conv_width: int = 0, k=None, v=None, k_scale=None, v_scale=None, cent=None,
+                 tail_k=None, tail_v=None, hist=None, block_table=None, row_state=None, free_pages=None, ring=None):
+        if kind not in CACHE_KINDS:
+            raise ValueError("kind must be one of %s, got %r" % (sorted(CACHE_KINDS), kind))
+        code, dt8 = CACHE_KINDS[kind]
+        P, H, B, d = n_pages, h_kv, block_size, head_dim
+        bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        want = dict(k=(dt8, (P, H, B, d)), v=(dt8, (P, H, B, d)), k_scale=(f32, (P, H)), v_scale=(f32, (P, H)),
+                    cent=(bf, (2, P, H, d)), tail_k=(bf, (rows, 2, H, B, d)), tail_v=(bf, (rows, 2, H, B, d)),
+                    hist=(bf, (rows, _CACHE_HIST, H, d)), block_table=(i32, (rows, max_blocks)),
+                    row_state=(i32, (rows, 2)), free_pages=(i32, (P,)), ring=(torch.int64, (2,)))
+        given = dict(k=k, v=v, k_scale=k_scale, v_scale=v_scale, cent=cent, tail_k=tail_k, tail_v=tail_v, hist=hist,
+                     block_table=block_table, row_state=row_state, free_pages=free_pages, ring=ring)
+        devs = set()
+        for n, x in given.items():
+            if x is None:
+                continue
+            _need(x, want[n][0], n)
+            if tuple(x.shape) != want[n][1]:
+                raise ValueError("%s must have shape %s, got %s" % (n, want[n][1], tuple(x.shape)))
+            devs.add(x.device)
+        if len(devs) != 1:
+            raise ValueError("the cache's tensors must be on one CUDA device")
+        self.rows, self.n_pages, self.max_blocks, self.h_kv = int(rows), int(n_pages), int(max_blocks), int(h_kv)
+        self.head_dim, self.block_size, self.kind, self.conv_width = int(d), int(B), kind, int(conv_width)
+        self.device = devs.pop()
+        for n, x in given.items():
+            setattr(self, n, x)
+        self.struct = CacheStruct(self.rows, self.n_pages, self.max_blocks, self.h_kv, self.head_dim, self.block_size,
+                                  code, self.conv_width, **{n: x.data_ptr() for n, x in given.items() if x is not None})
+        self._ref = ctypes.byref(self.struct)
+
+    def workspace_size(self, total_new: int, h_q: Optional[int] = None) -> int:
+        return int(lib().moba_cache_workspace_size(self._ref, int(total_new), int(h_q or self.h_kv)))
+
+    def alloc_workspace(self, total_new: int, h_q: Optional[int] = None) -> torch.Tensor:
+        return alloc_workspace(self.workspace_size(total_new, h_q), self.device)
+
+    def reset(self) -> None:
+        """Empties the cache (moba_cache_reset)."""
+        with _on(self.device):
+            _check(lib().moba_cache_reset(self._ref, _stream_of(self.device)), "moba_cache_reset")
+
+
+class _Here:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device):
+    """Makes `device` the current one for a launch."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _same_device(cache, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != cache.device:
+            raise ValueError("%s is on %s, the cache on %s" % (n, t.device, cache.device))
+
+
+def _need_shape(t, dtype, name, shape):
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+
+
+def alloc_cache(rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: int, block_size: int,
+                kind: str = "e4m3", conv_width: int = 0, device=None) -> Cache:
+    """An empty cache on ``device`` (default: the current CUDA device)."""
+    if kind not in CACHE_KINDS:
+        raise ValueError("kind must be one of %s, got %r" % (sorted(CACHE_KINDS), kind))
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    P, H, B, d = n_pages, h_kv, block_size, head_dim
+
+    def new(dtype, *shape):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    bf, f32, i32, dt8 = torch.bfloat16, torch.float32, torch.int32, CACHE_KINDS[kind][1]
+    c = Cache(rows=rows, n_pages=P, max_blocks=max_blocks, h_kv=H, head_dim=d, block_size=B, kind=kind,
+              conv_width=conv_width, k=new(dt8, P, H, B, d), v=new(dt8, P, H, B, d), k_scale=new(f32, P, H),
+              v_scale=new(f32, P, H), cent=new(bf, 2, P, H, d), tail_k=new(bf, rows, 2, H, B, d),
+              tail_v=new(bf, rows, 2, H, B, d), hist=new(bf, rows, _CACHE_HIST, H, d) if conv_width > 1 else None,
+              block_table=new(i32, rows, max_blocks), row_state=new(i32, rows, 2), free_pages=new(i32, P),
+              ring=new(torch.int64, 2))
+    c.reset()
+    return c
+
+
+def _plan_struct(cache, plan: CachePlan, total_new: int):
+    _need_shape(plan.cu_new, torch.int32, "plan.cu_new", (cache.rows + 1,))
+    for n, t in (("token_row", plan.token_row), ("token_pos", plan.token_pos), ("slot_map", plan.slot_map)):
+        _need_shape(t, torch.int32, "plan." + n, (total_new,))
+        _same_device(cache, **{"plan." + n: t})
+    _same_device(cache, **{"plan.cu_new": plan.cu_new})
+    return PlanStruct(total_new, plan.cu_new.data_ptr(), plan.token_row.data_ptr(), plan.token_pos.data_ptr(),
+                      plan.slot_map.data_ptr())
+
+
+def cache_tables(cache: Cache, new_len: torch.Tensor, total_new: int, row_state_out=None, ring_out=None,
+                 plan: Optional[CachePlan] = None, workspace=None) -> CachePlan:
+    """Pages and slots for ``new_len`` (int32 [rows]; -1 releases a row) new tokens, at most ``total_new`` in all
+    (moba_cache_tables).  Advances the cache's row_state and ring, or writes the state after the step to
+    ``row_state_out`` / ``ring_out``.  Returns the plan the other calls take."""
+    _need_shape(new_len, torch.int32, "new_len", (cache.rows,))
+    total_new = int(total_new)
+    if total_new < 0:
+        raise ValueError("total_new must not be negative")
+    if row_state_out is not None:
+        _need_shape(row_state_out, torch.int32, "row_state_out", (cache.rows, 2))
+    if ring_out is not None:
+        _need_shape(ring_out, torch.int64, "ring_out", (2,))
+    dev = cache.device
+    if plan is None:
+        plan = CachePlan(torch.empty(cache.rows + 1, dtype=torch.int32, device=dev),
+                         *(torch.empty(total_new, dtype=torch.int32, device=dev) for _ in range(3)))
+    ws = cache.alloc_workspace(0) if workspace is None else workspace
+    _same_device(cache, new_len=new_len, row_state_out=row_state_out, ring_out=ring_out, workspace=ws)
+    ps = _plan_struct(cache, plan, total_new)
+    with _on(dev):
+        rc = lib().moba_cache_tables(cache._ref, new_len.data_ptr(), _addr(row_state_out), _addr(ring_out),
+                                     ctypes.byref(ps), ws.data_ptr(), ws.numel(), _stream_of(dev))
+    _check(rc, "moba_cache_tables")
+    return plan
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def cache_append(cache: Cache, plan: CachePlan, k: torch.Tensor, v: torch.Tensor, conv_w=None, workspace=None) -> None:
+    """Writes the new keys and values [T, h_kv, d] bf16 into the cache, through the key conv when the cache has one
+    (``conv_w`` fp32 [h_kv, d, conv_width]) (moba_cache_append)."""
+    T = plan.token_row.shape[0]
+    shape = (T, cache.h_kv, cache.head_dim)
+    _need_shape(k, torch.bfloat16, "k", shape)
+    _need_shape(v, torch.bfloat16, "v", shape)
+    if (conv_w is not None) != (cache.conv_width > 0):
+        raise ValueError("conv_w must be given exactly when the cache has a key conv")
+    if conv_w is not None:
+        _need_shape(conv_w, torch.float32, "conv_w", (cache.h_kv, cache.head_dim, cache.conv_width))
+    ws = alloc_workspace(256, cache.device) if workspace is None else workspace
+    _same_device(cache, k=k, v=v, conv_w=conv_w, workspace=ws)
+    ps = _plan_struct(cache, plan, T)
+    with _on(cache.device):
+        rc = lib().moba_cache_append(cache._ref, ctypes.byref(ps), k.data_ptr(), v.data_ptr(), _addr(conv_w),
+                                     ws.data_ptr(), ws.numel(), _stream_of(cache.device))
+    _check(rc, "moba_cache_append")
+
+
+def cache_route(cache: Cache, plan: CachePlan, q: torch.Tensor, topk: int, workspace=None, sel_idx=None) -> torch.Tensor:
+    """The blocks of every new query: sel_idx int32 [T, h_q, topk] (moba_cache_route)."""
+    T = plan.token_row.shape[0]
+    _need(q, torch.bfloat16, "q", 3)
+    h_q = q.shape[1]
+    _need_shape(q, torch.bfloat16, "q", (T, h_q, cache.head_dim))
+    if sel_idx is None:
+        sel_idx = torch.empty((T, h_q, topk), dtype=torch.int32, device=cache.device)
+    _need_shape(sel_idx, torch.int32, "sel_idx", (T, h_q, topk))
+    ws = cache.alloc_workspace(T, h_q) if workspace is None else workspace
+    _same_device(cache, q=q, sel_idx=sel_idx, workspace=ws)
+    ps = _plan_struct(cache, plan, T)
+    with _on(cache.device):
+        rc = lib().moba_cache_route(cache._ref, ctypes.byref(ps), q.data_ptr(), h_q, int(topk), sel_idx.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), _stream_of(cache.device))
+    _check(rc, "moba_cache_route")
+    return sel_idx
+
+
+def cache_attention(cache: Cache, plan: CachePlan, q: torch.Tensor, sel_idx: Optional[torch.Tensor] = None,
+                    workspace=None, out=None, lse=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of the new queries over the blocks of ``sel_idx`` (cache_route's), or over all earlier tokens when it
+    is None.  Returns (out bf16 [T, h_q, d], lse fp32 [T, h_q]) (moba_cache_attention)."""
+    T = plan.token_row.shape[0]
+    _need(q, torch.bfloat16, "q", 3)
+    h_q = q.shape[1]
+    _need_shape(q, torch.bfloat16, "q", (T, h_q, cache.head_dim))
+    topk = 1
+    if sel_idx is not None:
+        _need(sel_idx, torch.int32, "sel_idx", 3)
+        topk = sel_idx.shape[2]
+        _need_shape(sel_idx, torch.int32, "sel_idx", (T, h_q, topk))
+    dev = cache.device
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((T, h_q), dtype=torch.float32, device=dev) if lse is None else lse
+    _need_shape(out, torch.bfloat16, "out", tuple(q.shape))
+    _need_shape(lse, torch.float32, "lse", (T, h_q))
+    ws = cache.alloc_workspace(T, h_q) if workspace is None else workspace
+    _same_device(cache, q=q, sel_idx=sel_idx, out=out, lse=lse, workspace=ws)
+    ps = _plan_struct(cache, plan, T)
+    with _on(dev):
+        rc = lib().moba_cache_attention(cache._ref, ctypes.byref(ps), q.data_ptr(), h_q, _addr(sel_idx), topk,
+                                        out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(dev))
+    _check(rc, "moba_cache_attention")
+    return out, lse

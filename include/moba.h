@@ -267,6 +267,156 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
                            const moba_shape* shape, const void* dk_conv, void* dk, float* dw, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Serving from a paged 8-bit cache
+ * ---------------------------------------------------------------------------
+ * MoBA for generation: keys and values of many requests ("rows") are held in
+ * pages of one MoBA block (B tokens), complete blocks in 8 bits.  Four calls,
+ * one after the other on one stream, serve a step (one token per request,
+ * several, or whole prompts):
+ *   moba_cache_tables     gives pages to the rows that grow, takes back those
+ *                         of finished rows, and lists the new tokens;
+ *   moba_cache_append     writes their keys and values (key conv included);
+ *   moba_cache_route      picks each new query's blocks from the centroids;
+ *   moba_cache_attention  attends to the picked blocks, or to all of them.
+ * Nothing is read back to the host, so a step can be captured into a graph.
+ *
+ * The buffers (device memory of the caller, 16-byte aligned; contents set by
+ * moba_cache_reset and the calls above).  Element order is row-major.
+ *  k, v          8 bits [n_pages, h_kv, B, d]: complete blocks.  kind 0: e4m3,
+ *                kind 1: int8; the value held is x8 * scale
+ *  k_scale, v_scale  fp32 [n_pages, h_kv]: max(amax / M, 2^-126) over the
+ *                block's B x d values, M = 448 (e4m3) or 127 (int8)
+ *  cent          bf16 [2, n_pages, h_kv, d]: the mean of a complete block's
+ *                bf16 keys as hi + lo (hi = bf16(c), lo = bf16(c - hi))
+ *  tail_k, tail_v  bf16 [rows, 2, h_kv, B, d]: the tokens of a row's last two
+ *                blocks, block j in bank j mod 2.  A partial block is read
+ *                from here.  Because both are kept, a row's length may be
+ *                set back by up to B tokens (rejected drafts); with a key
+ *                conv by at most 17 - conv_width
+ *  hist          bf16 [rows, 16, h_kv, d]: the last raw keys, position p at
+ *                p mod 16 (NULL allowed when conv_width <= 1)
+ *  block_table   int32 [rows, max_blocks]: the page of each block of a row;
+ *                entries from the row's page count on are stale
+ *  row_state     int32 [rows, 2]: tokens held, pages held
+ *  free_pages    int32 [n_pages]: ring of free pages; ring: int64 [2], the
+ *                ring's first entry and its end (both count up; mod n_pages)
+ *
+ * h_q, head_dim, block_size, topk and conv_width have the limits of the other
+ * calls; max_blocks * B, n_pages * B and T * h_q * max(d, topk) are < 2^31.
+ * Offsets into the pages are 64 bits wide.
+ */
+#define MOBA_CACHE_E4M3 0
+#define MOBA_CACHE_INT8 1
+
+/* Further bits of the device status word (moba_check_status). */
+#define MOBA_STATUS_NO_PAGES 16   /* a row was refused: no free pages, or more than max_blocks blocks */
+#define MOBA_STATUS_BAD_TABLE 32  /* a row state, page number or plan entry out of range; skipped */
+#define MOBA_STATUS_NONFINITE 64  /* a NaN or infinite key or value was stored as 0 */
+
+typedef struct moba_cache {
+  int32_t rows;       /* requests the cache has room for */
+  int32_t n_pages;
+  int32_t max_blocks; /* width of the block table */
+  int32_t h_kv;
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t block_size; /* 16, 32, 64 or 128 */
+  int32_t kind;       /* MOBA_CACHE_E4M3 or MOBA_CACHE_INT8 */
+  int32_t conv_width; /* 0 (no key conv) .. 8 */
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  void* cent;
+  void* tail_k;
+  void* tail_v;
+  void* hist;
+  int32_t* block_table;
+  int32_t* row_state;
+  int32_t* free_pages;
+  int64_t* ring;
+} moba_cache;
+
+/* The new tokens of a step, packed row after row: written by
+ * moba_cache_tables, read by the other calls.  total_new (host value) is the
+ * capacity T of the token arrays; entries behind cu_new[rows] are padding
+ * (row, position and slot -1). */
+typedef struct moba_cache_plan {
+  int32_t total_new;
+  int32_t* cu_new;    /* [rows + 1] first new token of each row */
+  int32_t* token_row; /* [T] */
+  int32_t* token_pos; /* [T] position in the row; -1: the row was refused */
+  int32_t* slot_map;  /* [T] page * B + position mod B; -1: not stored */
+} moba_cache_plan;
+
+/* Bytes of device workspace that any of the calls below needs for a step of
+ * total_new tokens and h_q query heads (0: invalid).  As elsewhere it needs
+ * no initialisation, its first word is the status word, and calls whose work
+ * can overlap on the GPU need a workspace each. */
+size_t moba_cache_workspace_size(const moba_cache* cache, int total_new, int h_q);
+
+/* Empties the cache: no tokens, every page free, tails and history zero. */
+int moba_cache_reset(const moba_cache* cache, void* stream);
+
+/*
+ * Block tables and slot maps.  new_len: int32 [rows], the tokens each row is
+ * about to get; -1 gives the row's pages back and empties it (they can be
+ * taken from the next call on).
+ *
+ * Row r needs max(0, ceil((L + n) / B) - pages held) pages.  They are taken
+ * from the ring in row order.  A row is served if all pages needed by rows up
+ * to and including it are there; one that is not served (also: more than
+ * max_blocks blocks; more than T tokens up to and including it) keeps its
+ * state, its tokens get position and slot -1, and MOBA_STATUS_NO_PAGES is set
+ * (BAD_SEQLENS for the tokens beyond T, which are not listed).
+ *
+ * row_state_out, ring_out: where the state after the step goes; the cache's
+ * own buffers for the usual step in place (then NULL may be given), others to
+ * plan a step that can be planned again.  Block table and ring entries are
+ * written in place; planning a step again writes the same ones.
+ */
+int moba_cache_tables(const moba_cache* cache, const int32_t* new_len, int32_t* row_state_out, int64_t* ring_out,
+                      const moba_cache_plan* plan, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Writes the new tokens.  row_state is the state after moba_cache_tables.
+ *  k, v     bf16 [T, h_kv, d]; conv_w fp32 [h_kv, d, conv_width] (NULL at 0)
+ * Keys pass through the key conv (k' = bf16(k + SiLU(sum_l w_l (.) k_{t-l})),
+ * summed in 64 bits, with the raw keys before the step from hist).  A block
+ * that becomes complete is rounded to 8 bits from its bf16 tokens, once:
+ * x / scale to the nearest value, ties to even.  NaN and infinities are
+ * stored as 0 (MOBA_STATUS_NONFINITE).  Tokens with slot -1 are skipped.
+ */
+int moba_cache_append(const moba_cache* cache, const moba_cache_plan* plan, const void* k, const void* v,
+                      const float* conv_w, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Routing of the new queries over the cached centroids: as in moba_forward,
+ * the topk - 1 earlier blocks with the largest q . (hi + lo) and the own
+ * block.  Scores are compared exactly (as if summed in 64 bits; a NaN score
+ * counts as -infinity); equal scores keep the lower block.
+ *  q        bf16 [T, h_q, d];  sel_idx int32 [T, h_q, topk] (output, ascending,
+ *           own block last, then -1).  Rows of tokens with position -1 are all
+ *           -1; rows of padding tokens stay as they were.
+ */
+int moba_cache_route(const moba_cache* cache, const moba_cache_plan* plan, const void* q, int h_q, int topk,
+                     int32_t* sel_idx, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of the new queries over the cache: softmax(q . k / sqrt(d)) v over
+ * the tokens at positions <= the query's, of the blocks listed in sel_idx
+ * (moba_cache_route's; ascending, an entry that is not above the one before it
+ * or is beyond the own block is skipped with MOBA_STATUS_BAD_SEL_IDX), or of
+ * all blocks when sel_idx is NULL (topk is then ignored).
+ *  out bf16 [T, h_q, d];  lse fp32 [T, h_q].  A query that sees no token
+ *  (position -1, or no valid entry) gets out 0 and lse -infinity; rows of
+ *  padding tokens stay as they were.
+ */
+int moba_cache_attention(const moba_cache* cache, const moba_cache_plan* plan, const void* q, int h_q,
+                         const int32_t* sel_idx, int topk, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads the status word the last call on this
  * workspace left.  *device_status receives the MOBA_STATUS_* bits (0 = ok).
  * Returns MOBA_OK, MOBA_EDEVICE if any bit is set, or MOBA_ELAUNCH if the

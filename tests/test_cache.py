@@ -1,0 +1,246 @@
+"""The paged 8-bit cache: tables, append, routing and attention, alone and as a serving run, against a plain 64-bit
+cache (cache_ref.py).  Bookkeeping, 8-bit codes, scales, centroids, tails and selections are compared bit for bit."""
+import ctypes
+
+import pytest
+import torch
+
+import cache_ref as cr
+from block_sparse_long_key_b200 import build, moba
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------ host checks (CPU)
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return moba.lib()
+
+
+FAKE = 1 << 20  # a 16- and 256-byte aligned address that the checks never follow
+
+
+def _struct(**kw):
+    base = dict(rows=4, n_pages=64, max_blocks=16, h_kv=2, head_dim=64, block_size=32, kind=0, conv_width=0)
+    base.update({n: FAKE for n in ("k", "v", "k_scale", "v_scale", "cent", "tail_k", "tail_v", "block_table",
+                                   "row_state", "free_pages", "ring")})
+    base.update(kw)
+    return moba.CacheStruct(**base)
+
+
+def _plan(**kw):
+    base = dict(total_new=4, cu_new=FAKE, token_row=FAKE, token_pos=FAKE, slot_map=FAKE)
+    base.update(kw)
+    return moba.PlanStruct(**base)
+
+
+@pytest.mark.parametrize("bad", [dict(head_dim=96), dict(block_size=48), dict(kind=2), dict(conv_width=9),
+                                 dict(conv_width=-1), dict(rows=0), dict(n_pages=0), dict(max_blocks=0), dict(h_kv=0),
+                                 dict(n_pages=1 << 26), dict(max_blocks=1 << 26)], ids=str)
+def test_bad_cache_sizes_are_refused(L, bad):
+    c, p = _struct(**bad), _plan()
+    ref, pr = ctypes.byref(c), ctypes.byref(p)
+    assert L.moba_cache_workspace_size(ref, 4, 2) == 0
+    assert L.moba_cache_reset(ref, None) == moba.MOBA_EINVAL
+    assert L.moba_cache_tables(ref, FAKE, None, None, pr, FAKE, 1 << 30, None) == moba.MOBA_EINVAL
+    assert L.moba_cache_append(ref, pr, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == moba.MOBA_EINVAL
+    assert L.moba_cache_route(ref, pr, FAKE, 2, 4, FAKE, FAKE, 1 << 30, None) == moba.MOBA_EINVAL
+    assert L.moba_cache_attention(ref, pr, FAKE, 2, None, 1, FAKE, FAKE, FAKE, 1 << 30, None) == moba.MOBA_EINVAL
+
+
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "cent", "tail_k", "tail_v", "block_table",
+                                  "row_state"])
+def test_missing_and_misaligned_buffers_are_refused(L, name):
+    p = _plan()
+    for value, rc in ((None, moba.MOBA_EINVAL), (FAKE + 8, moba.MOBA_EALIGN)):
+        c = _struct(**{name: value})
+        ref, pr = ctypes.byref(c), ctypes.byref(p)
+        assert L.moba_cache_reset(ref, None) == rc
+        assert L.moba_cache_append(ref, pr, FAKE, FAKE, None, FAKE, 1 << 30, None) == rc
+        assert L.moba_cache_attention(ref, pr, FAKE, 2, None, 1, FAKE, FAKE, FAKE, 1 << 30, None) == rc
+
+
+def test_call_arguments_are_refused(L):
+    c, p = _struct(), _plan()
+    ref, pr = ctypes.byref(c), ctypes.byref(p)
+    E, A, W = moba.MOBA_EINVAL, moba.MOBA_EALIGN, moba.MOBA_EWORKSPACE
+    big = 1 << 40
+    assert L.moba_cache_tables(ref, None, None, None, pr, FAKE, big, None) == E
+    assert L.moba_cache_tables(ref, FAKE, FAKE + 4, None, pr, FAKE, big, None) == A
+    assert L.moba_cache_tables(ref, FAKE, None, None, pr, FAKE, 256, None) == W
+    assert L.moba_cache_tables(ref, FAKE, None, None, pr, FAKE + 128, big, None) == A
+    assert L.moba_cache_tables(ref, FAKE, None, None, None, FAKE, big, None) == E
+    for field in ("cu_new", "token_row", "token_pos", "slot_map"):
+        q = _plan(**{field: None})
+        assert L.moba_cache_tables(ref, FAKE, None, None, ctypes.byref(q), FAKE, big, None) == E
+        assert L.moba_cache_route(ref, ctypes.byref(q), FAKE, 2, 4, FAKE, FAKE, big, None) == E
+    neg = _plan(total_new=-1)
+    assert L.moba_cache_append(ref, ctypes.byref(neg), FAKE, FAKE, None, FAKE, big, None) == E
+    assert L.moba_cache_append(ref, pr, None, FAKE, None, FAKE, big, None) == E
+    conv = _struct(conv_width=4, hist=FAKE)
+    assert L.moba_cache_append(ctypes.byref(conv), pr, FAKE, FAKE, None, FAKE, big, None) == E
+    nohist = _struct(conv_width=4)
+    assert L.moba_cache_append(ctypes.byref(nohist), pr, FAKE, FAKE, FAKE, FAKE, big, None) == E
+    for hq, topk in ((3, 4), (0, 4), (2, 0), (2, 65)):
+        assert L.moba_cache_route(ref, pr, FAKE, hq, topk, FAKE, FAKE, big, None) == E
+        assert L.moba_cache_attention(ref, pr, FAKE, hq, FAKE, topk, FAKE, FAKE, FAKE, big, None) == E
+    assert L.moba_cache_route(ref, pr, FAKE, 2, 4, FAKE + 4, FAKE, big, None) == A
+    assert L.moba_cache_route(ref, pr, FAKE, 2, 4, FAKE, FAKE, 255, None) == W
+    assert L.moba_cache_attention(ref, pr, FAKE, 2, None, 1, None, FAKE, FAKE, big, None) == E
+    huge = _plan(total_new=1 << 24)
+    assert L.moba_cache_attention(ref, ctypes.byref(huge), FAKE, 2, None, 1, FAKE, FAKE, FAKE, big, None) == E
+    assert L.moba_cache_workspace_size(ref, 1 << 24, 2) == 0
+    none = _plan(total_new=0, token_row=None, token_pos=None, slot_map=None)  # nothing to do: nothing launched
+    assert L.moba_cache_append(ref, ctypes.byref(none), None, None, None, None, 0, None) == moba.MOBA_OK
+    assert L.moba_cache_route(ref, ctypes.byref(none), None, 2, 4, None, None, 0, None) == moba.MOBA_OK
+    assert L.moba_cache_attention(ref, ctypes.byref(none), None, 2, None, 1, None, None, None, 0, None) == moba.MOBA_OK
+
+
+def test_binding_refuses_host_tensors_and_kinds():
+    with pytest.raises(TypeError):
+        moba.Cache(rows=1, n_pages=4, max_blocks=4, h_kv=1, head_dim=64, block_size=16,
+                   block_table=torch.zeros((1, 4), dtype=torch.int32))
+    with pytest.raises(ValueError):
+        moba.Cache(rows=1, n_pages=4, max_blocks=4, h_kv=1, head_dim=64, block_size=16, kind="e5m2")
+    with pytest.raises(ValueError):
+        moba.Cache(rows=1, n_pages=4, max_blocks=4, h_kv=1, head_dim=64, block_size=16)
+
+
+# ---------------------------------------------------------------------------------------------------- serving runs (GPU)
+class Run:
+    """A cache on the GPU and the plain one beside it."""
+
+    def __init__(self, rows, n_pages, max_blocks, h_q, h_kv, d, B, kind, W, topk, seed=0, scale=1.0):
+        self.c = moba.alloc_cache(rows, n_pages, max_blocks, h_kv, d, B, kind=kind, conv_width=W)
+        # what was never written is never read: NaN scales and pages of NaN codes
+        self.c.k.view(torch.uint8).fill_(0x7F), self.c.v.view(torch.uint8).fill_(0x7F)
+        for x in (self.c.k_scale, self.c.v_scale, self.c.cent, self.c.tail_k, self.c.tail_v):
+            x.fill_(float("nan"))
+        self.ref = cr.RefCache(rows, n_pages, max_blocks, h_kv, d, B, kind, W)
+        self.hq, self.topk, self.scale = h_q, topk, scale
+        self.gen = torch.Generator().manual_seed(seed)
+        self.w = torch.rand((h_kv, d, W), generator=self.gen) - 0.5 if W else None
+
+    def rand(self, *shape):
+        return (self.scale * torch.randn(shape, generator=self.gen)).to(torch.bfloat16)
+
+    def tables(self, new_len, pad=0, total=None):
+        T = (sum(max(n, 0) for n in new_len) if total is None else total) + pad
+        ws = self.c.alloc_workspace(T, self.hq)
+        plan = moba.cache_tables(self.c, torch.tensor(new_len, dtype=torch.int32, device="cuda"), T, workspace=ws)
+        status = moba.check_status(ws)
+        want = self.ref.tables(new_len, T)
+        for got, exp, name in zip(plan, want, ("cu", "row", "pos", "slot")):
+            assert got.tolist() == exp, name
+        self.check_state()
+        return plan, want, status
+
+    def check_state(self):
+        r = self.ref
+        assert self.c.row_state.tolist() == [[a, len(b)] for a, b in zip(r.length, r.pages)]
+        table = self.c.block_table.tolist()
+        for i in range(r.rows):
+            assert table[i][:len(r.pages[i])] == r.pages[i]
+        head, tail = self.c.ring.tolist()
+        ring = self.c.free_pages.tolist()
+        assert [ring[i % r.n_pages] for i in range(head, tail)] == list(r.free)
+
+    def append(self, plan, want, k=None, v=None):
+        T = plan.token_row.shape[0]
+        r = self.ref
+        k = self.rand(T, r.h, r.d) if k is None else k
+        v = self.rand(T, r.h, r.d) if v is None else v
+        ws = self.c.alloc_workspace(T, self.hq)
+        moba.cache_append(self.c, plan, k.cuda(), v.cuda(), conv_w=None if self.w is None else self.w.cuda(),
+                          workspace=ws)
+        status = moba.check_status(ws)
+        r.append(want[0], want[4], k, v, self.w)
+        return status
+
+    def check_store(self, rows=None):
+        r = self.ref
+        k8, v8 = self.c.k.view(torch.uint8).cpu(), self.c.v.view(torch.uint8).cpu()
+        ks, vs, cent = self.c.k_scale.cpu(), self.c.v_scale.cpu(), self.c.cent.cpu()
+        tk, tv = self.c.tail_k.cpu(), self.c.tail_v.cpu()
+        for i in range(r.rows) if rows is None else rows:
+            for j in range(r.length[i] // r.B):
+                pg = r.pages[i][j]
+                for x, codes, scales, what in ((r.key, k8, ks, "k"), (r.val, v8, vs, "v")):
+                    c, s = r.block(x, i, j)
+                    assert torch.equal(scales[pg], s), (what, i, j)
+                    a, b = codes[pg], c.view(torch.uint8)
+                    if r.kind == "e4m3":   # +0 and -0 are one value
+                        a, b = torch.where(a == 128, 0, a), torch.where(b == 128, 0, b)
+                    assert torch.equal(a, b), (what, i, j)
+                hi, lo = r.centroid(i, j)
+                assert torch.equal(cent[0, pg], hi) and torch.equal(cent[1, pg], lo), (i, j)
+            left, j = r.length[i] % r.B, r.length[i] // r.B
+            if left:
+                assert torch.equal(tk[i, j % 2, :, :left].transpose(0, 1), r.key[i][j * r.B:]), i
+                assert torch.equal(tv[i, j % 2, :, :left].transpose(0, 1), r.val[i][j * r.B:]), i
+
+    def queries(self, plan, want, q=None, dense=True):
+        T = plan.token_row.shape[0]
+        r = self.ref
+        q = self.rand(T, self.hq, r.d) if q is None else q
+        ws = self.c.alloc_workspace(T, self.hq)
+        sel0 = torch.full((T, self.hq, self.topk), -7, dtype=torch.int32, device="cuda")
+        sel = moba.cache_route(self.c, plan, q.cuda(), self.topk, workspace=ws, sel_idx=sel0)
+        assert moba.check_status(ws) == 0
+        row, pos = want[1], want[2]
+        exp = r.route(row, pos, q, self.topk)
+        real = torch.tensor([x >= 0 for x in row])
+        assert torch.equal(sel.cpu()[real], exp[real])
+        assert (sel.cpu()[~real] == -7).all()          # padding rows stay as they were
+        for s_gpu, s_ref in ((sel, exp), (None, None))[:2 if dense else 1]:
+            out = torch.full((T, self.hq, r.d), 7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((T, self.hq), 7.0, device="cuda")
+            ws.random_(0, 255)
+            moba.cache_attention(self.c, plan, q.cuda(), sel_idx=s_gpu, workspace=ws, out=out, lse=lse)
+            assert moba.check_status(ws) == 0
+            ref = r.attend(row, pos, q, s_ref)
+            cr.check_attention(out.cpu()[real], lse.cpu()[real], [x[real] for x in ref], r.d,
+                               "all" if s_ref is None else "selected")
+            assert (out.cpu()[~real] == 7).all() and (lse.cpu()[~real] == 7).all()
+        return sel
+
+    def step(self, new_len, pad=0, dense=True):
+        plan, want, st = self.tables(new_len, pad)
+        assert st == 0
+        if plan.token_row.shape[0]:
+            assert self.append(plan, want) == 0
+            self.check_store()
+            self.queries(plan, want, dense=dense)
+
+
+# (h_q, h_kv, d, B, kind, conv width, topk)
+SHAPES = [
+    (2, 2, 64, 32, "e4m3", 4, 4),
+    (4, 1, 64, 16, "int8", 3, 3),
+    (6, 2, 128, 64, "e4m3", 0, 2),
+    (8, 4, 128, 16, "int8", 8, 64),
+    (1, 1, 64, 128, "int8", 2, 1),
+    (5, 5, 128, 128, "e4m3", 1, 3),
+    (24, 1, 64, 32, "e4m3", 0, 5),
+]
+
+
+def _ids(s):
+    return "h%dx%d_d%d_B%d_%s_w%d_k%d" % s
+
+
+@gpu
+@pytest.mark.parametrize("shape", SHAPES, ids=_ids)
+def test_serving_run(shape):
+    """Prompts, single tokens, chunks across blocks, idle rows, a finished row and its successor, padding."""
+    hq, h, d, B, kind, W, topk = shape
+    r = Run(5, 400 // B + 40, 600 // B + 6, hq, h, d, B, kind, W, topk, seed=B + d)
+    r.step([B * 3 + 5, 1, 0, B, 2 * B - 1], pad=3)
+    r.step([1, 1, 1, 1, 1])
+    r.step([1, 0, 2, 0, 1], pad=2)
+    r.step([3, B, -1, 2 * B + 3, 7])
+    r.step([0, 0, B + 1, 0, 0])
+    r.step([4 * B + 2, 9, 17, 2, 1], pad=1)
+    for _ in range(3):
+        r.step([1, 1, 1, 1, 1])
