@@ -33,7 +33,7 @@ bool sizes_ok(const moba_cache* c) {
 }
 
 bool step_ok(const moba_cache* c, int total_new, int h_q, int topk) {
-  if (total_new < 0 || h_q < 1 || h_q % c->h_kv != 0 || topk < 1 || topk > 64) return false;
+  if (total_new < 0 || h_q < 1 || h_q > 65535 || h_q % c->h_kv != 0 || topk < 1 || topk > 64) return false;
   const long long widest = c->head_dim > topk ? c->head_dim : topk;
   return (long long)total_new * h_q * widest < (1LL << 31);
 }

@@ -84,7 +84,7 @@ __device__ void encode_block(const View& c, const bf16* tile, uint8_t* dst, floa
   __syncthreads();
   m = red[0];
   for (int i = 1; i < kThreads / 32; ++i) m = fmaxf(m, red[i]);
-  const float s = fmaxf(__fdiv_rn(m, KIND == 0 ? 448.f : 127.f), 1.17549435e-38f);
+  const float s = fmaxf(m * (KIND == 0 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f);
   const size_t at = (size_t)pg * c.h_kv + head;
   for (int i = tid; i < n; i += kThreads) dst[at * n + i] = encode8<KIND>(__bfloat162float(tile[i]), s);
   if (tid == 0) scale[at] = s;

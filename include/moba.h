@@ -286,8 +286,9 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  * moba_cache_reset and the calls above).  Element order is row-major.
  *  k, v          8 bits [n_pages, h_kv, B, d]: complete blocks.  kind 0: e4m3,
  *                kind 1: int8; the value held is x8 * scale
- *  k_scale, v_scale  fp32 [n_pages, h_kv]: max(amax / M, 2^-126) over the
- *                block's B x d values, M = 448 (e4m3) or 127 (int8)
+ *  k_scale, v_scale  fp32 [n_pages, h_kv]: max(amax * r, 2^-126) over the
+ *                block's B x d values, r = the fp32 nearest 1/448 (e4m3) or
+ *                1/127 (int8)
  *  cent          bf16 [2, n_pages, h_kv, d]: the mean of a complete block's
  *                bf16 keys as hi + lo (hi = bf16(c), lo = bf16(c - hi))
  *  tail_k, tail_v  bf16 [rows, 2, h_kv, B, d]: the tokens of a row's last two
@@ -303,8 +304,8 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  *  free_pages    int32 [n_pages]: ring of free pages; ring: int64 [2], the
  *                ring's first entry and its end (both count up; mod n_pages)
  *
- * h_q, head_dim, block_size, topk and conv_width have the limits of the other
- * calls; max_blocks * B, n_pages * B and T * h_q * max(d, topk) are < 2^31.
+ * h_q (at most 65535), head_dim, block_size, topk and conv_width have the
+ * limits of the other calls; max_blocks * B, n_pages * B and T * h_q * max(d, topk) are < 2^31.
  * Offsets into the pages are 64 bits wide.
  */
 #define MOBA_CACHE_E4M3 0

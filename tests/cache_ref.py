@@ -90,7 +90,7 @@ class RefCache:
     def block(self, x, r, j):
         """(codes, scale) of complete block j of a row's keys or values: [h, B, d], [h]."""
         t = x[r][j * self.B:(j + 1) * self.B].float().transpose(0, 1)
-        s = (t.abs().amax((1, 2)) / QMAX[self.kind]).clamp_min(2.0 ** -126)
+        s = (t.abs().amax((1, 2)) * (torch.tensor(1.0) / QMAX[self.kind])).clamp_min(2.0 ** -126)
         y = t / s[:, None, None]
         if self.kind == "e4m3":
             return y.clamp(-448, 448).to(torch.float8_e4m3fn), s
