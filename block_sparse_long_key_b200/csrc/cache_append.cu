@@ -4,12 +4,13 @@
 //   block complete: s = max(amax r, 2^-126), x8 = rn(x / s); c = mean k', hi = bf16(c), lo = bf16(c - hi)
 //   else: bf16 tail
 //
-// The unit of work is a run: the new tokens of one row inside one block.  One
-// CTA of 128 threads per (run, KV head); a thread holds 8 channels of
-// consecutive tokens of the block in registers (NCH = B d / 1024 pieces of 16
-// bytes), so a complete block is read once (its earlier tokens from the tail),
-// its largest magnitude agreed on, and its codes written once.  Bound by HBM
-// for prompts, by latency for single tokens.
+// The unit of work is a run: the new tokens of one row inside one block.  A
+// CTA takes a run for some KV heads in turn, the next head's tokens on their
+// way (cp.async) while one is rounded.  A thread holds 8 channels of NCH
+// consecutive tokens of the block in registers, so a complete block is read
+// once (its earlier tokens from the tail), its largest magnitudes agreed on,
+// and its codes written once.  Bound by HBM for prompts, by latency for single
+// tokens.
 //
 // A row's first run is the only one that may need what the step replaces: the
 // tail bank of its block (its earlier tokens) and the raw-key history.  Its
@@ -31,8 +32,6 @@
 namespace moba {
 namespace cache {
 namespace {
-
-constexpr int kThreads = 128;
 
 struct RowInfo {
   int row, t_begin;  // the row's first new token
@@ -151,73 +150,70 @@ __device__ __forceinline__ uint2 encode8(uint4 u, float s, float r, bool divide)
   return o;
 }
 
-struct Shared {
-  float red[kThreads / 32];
-  double sum[kThreads * 8];  // block sums of the token groups
+// Threads and pieces of 16 bytes per thread for a tile of B tokens x D channels.
+template <int D, int BLK>
+struct Shape {
+  static constexpr int THREADS = BLK * D >= 8192 ? 256 : 128;
+  static constexpr int NCH = BLK * D / 8 / THREADS;
+  static constexpr int LANES = D / 8;               // threads across a token
+  static constexpr int GROUPS = THREADS / LANES;    // token groups of NCH consecutive tokens
+  static constexpr int STAGE = 2 * NCH * THREADS;   // 16-byte slots of one head's K and V
+  static constexpr int BYTES = 2 * STAGE * 16 + THREADS * 8 * 8;
+  static_assert(NCH * GROUPS == BLK, "tile");
 };
 
-// Codes, scale (and centroid) of a complete block held in registers.
-template <int KIND, int D, int NCH, bool KEY>
-__device__ __forceinline__ void write_block(const View& c, uint4* x, int pg, int head, Shared& sh) {
-  constexpr int LANES = D / 8, GROUPS = kThreads / LANES, B = NCH * GROUPS;
-  const int tid = threadIdx.x, ck = tid % LANES, grp = tid / LANES;
-  __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+template <int NCH>
+__device__ __forceinline__ float amax8(const uint4* x) {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x[i]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m2 = __hmax2(m2, __habs2(h[e]));
+    for (int e = 0; e < 4; ++e) m = __hmax2_nan(m, __habs2(h[e]));
   }
-  float m = fmaxf(__low2float(m2), __high2float(m2));
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
-  if ((tid & 31) == 0) sh.red[tid >> 5] = m;
-  if constexpr (KEY) {
-    double s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.0;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      float f[8];
-      bf16x8_to_f32(x[i], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += (double)f[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sh.sum[(grp * 8 + e) * LANES + ck] = s[e];
-  }
-  __syncthreads();
-  m = fmaxf(fmaxf(sh.red[0], sh.red[1]), fmaxf(sh.red[2], sh.red[3]));
-  const float s = fmaxf(m * (KIND == 0 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f);
-  const float r = __frcp_rn(s);
-  const bool divide = s < 8.6736174e-19f;  // 2^-60
-  const size_t at = (size_t)pg * c.h_kv + head;
-  uint8_t* dst = (KEY ? c.k : c.v) + at * (B * D) + ck * 8;
-#pragma unroll
-  for (int i = 0; i < NCH; ++i)
-    *reinterpret_cast<uint2*>(dst + (grp * NCH + i) * D) = encode8<KIND>(x[i], s, r, divide);
-  if (tid == 0) (KEY ? c.k_scale : c.v_scale)[at] = s;
-  if constexpr (KEY) {
-    if (tid < D) {
-      double t = 0.0;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) t += sh.sum[(g * 8 + (tid & 7)) * LANES + tid / 8];
-      const float mean = (float)(t * (1.0 / B));
-      const bf16 hi = __float2bfloat16_rn(mean);
-      c.cent[at * D + tid] = hi;
-      c.cent[((size_t)c.n_pages * c.h_kv + at) * D + tid] = __float2bfloat16_rn(mean - __bfloat162float(hi));
-    }
-  }
-  __syncthreads();
+  const float a = __low2float(m), b = __high2float(m);
+  return a > b || a != a ? a : b;  // NaN stays
 }
 
-template <int KIND, int D, int NCH, bool CONV>
-__global__ void __launch_bounds__(kThreads)
+// Largest magnitude; NaN and infinities, if any, become zero first.
+template <int NCH>
+__device__ __forceinline__ float finite_amax(uint4* x, bool* bad) {
+  float m = amax8<NCH>(x);
+  if (!(m <= 3.4e38f)) {
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) x[i] = finite8(x[i], bad);
+    m = amax8<NCH>(x);
+  }
+  return m;
+}
+
+template <int KIND, int D, int BLK>
+__device__ __forceinline__ void write_codes(uint8_t* dst, const uint4* x, float s) {
+  using S = Shape<D, BLK>;
+  const float r = __frcp_rn(s);
+  const bool divide = s < 8.6736174e-19f;  // 2^-60
+  dst += (threadIdx.x / S::LANES * S::NCH) * D + threadIdx.x % S::LANES * 8;
+#pragma unroll
+  for (int i = 0; i < S::NCH; ++i) *reinterpret_cast<uint2*>(dst + i * D) = encode8<KIND>(x[i], s, r, divide);
+}
+
+template <int KIND>
+__device__ __forceinline__ float scale_of(float m) {
+  return fmaxf(m * (KIND == 0 ? 1.f / 448.f : 1.f / 127.f), 1.17549435e-38f);
+}
+
+template <int KIND, int D, int BLK, bool CONV>
+__global__ void __launch_bounds__(Shape<D, BLK>::THREADS)
 append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict__ v, const float* __restrict__ w,
-              int per_token, int32_t* status) {
-  constexpr int LANES = D / 8, GROUPS = kThreads / LANES, B = NCH * GROUPS;
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, head = blockIdx.y, u = blockIdx.x;
+              int per_token, int heads_per_cta, int32_t* status) {
+  using S = Shape<D, BLK>;
+  constexpr int THREADS = S::THREADS, NCH = S::NCH, LANES = S::LANES, GROUPS = S::GROUPS, B = BLK;
+  extern __shared__ __align__(16) unsigned char smem[];
+  uint4* ring = reinterpret_cast<uint4*>(smem);                            // [2][K, V][NCH][THREADS]
+  double* gsum = reinterpret_cast<double*>(smem + 2 * S::STAGE * 16);      // [GROUPS][8][LANES]
+  __shared__ float red[2][THREADS / 32];
+  const int tid = threadIdx.x, u = blockIdx.x;
+  const int head0 = blockIdx.y * heads_per_cta, head1 = min(c.h_kv, head0 + heads_per_cta);
   const int ch = tid % LANES * 8, off0 = tid / LANES * NCH;  // this thread's channels and first token of a block
   const int total = min(__ldg(p.cu + c.rows), p.T);
   // ---- which run
@@ -267,15 +263,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
   }
   const bool has_old = R.pos0 % B != 0;
   bool bad = false;
-  auto new_key = [&](int rel) {
-    uint4 x;
-    if constexpr (CONV) x = conv8<D>(c, R, k, w, head, ch, rel);
-    else x = raw_key<D>(c, R, k, head, ch, rel);
-    return finite8(x, &bad);
-  };
-  auto new_val = [&](int rel) {
-    return finite8(__ldg(reinterpret_cast<const uint4*>(v + ((size_t)(R.t_begin + rel) * c.h_kv + head) * D + ch)), &bad);
-  };
+
   for (int j = j0; j <= j1; ++j) {
     const int lo = max(R.pos0 - j * B, 0), hi = min(R.len - j * B, B);  // new tokens inside the block
     const int rel0 = j * B - R.pos0;
@@ -287,90 +275,159 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
       if (slot >= 0 && slot / B < c.n_pages) pg = slot / B;
       else if (tid == 0) set_status(status, kStatusBadTable);
     }
-    uint4 x[NCH];
+    // Copies of a head's tokens on their way: a thread reads only the slots that it fills itself.
+    auto fetch = [&](int head) {
+      if (head < head1) {
+        uint4* dst = ring + ((head - head0) & 1) * S::STAGE + tid;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int off = off0 + i;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (off < lo) {
-        if (pg >= 0) x[i] = *tail_at<D>(c.tail_k, c, R.row, j, head, off, ch);
-      } else if (off < hi) {
-        x[i] = new_key(rel0 + off);
-      }
-    }
-    if (keep) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (off0 + i >= lo && off0 + i < hi) *tail_at<D>(c.tail_k, c, R.row, j, head, off0 + i, ch) = x[i];
-    }
-    if (pg >= 0) write_block<KIND, D, NCH, true>(c, x, pg, head, sh);
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int off = off0 + i;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (off < lo) {
-        if (pg >= 0) x[i] = *tail_at<D>(c.tail_v, c, R.row, j, head, off, ch);
-      } else if (off < hi) {
-        x[i] = new_val(rel0 + off);
-      }
-    }
-    if (keep) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (off0 + i >= lo && off0 + i < hi) *tail_at<D>(c.tail_v, c, R.row, j, head, off0 + i, ch) = x[i];
-    }
-    if (pg >= 0) write_block<KIND, D, NCH, false>(c, x, pg, head, sh);
-  }
-  if (is_first) {
-    if (has_old) {
-      int jc = j_last;  // the later one of the last two blocks in the first block's bank
-      if ((jc ^ j_first) & 1) --jc;
-      if (jc > j_first) {
-        __syncthreads();  // the earlier tokens have been read
-        const int hi = min(R.len - jc * B, B), rel0 = jc * B - R.pos0;
-        for (int off = off0; off < min(off0 + NCH, hi); ++off) {
-          *tail_at<D>(c.tail_k, c, R.row, jc, head, off, ch) = new_key(rel0 + off);
-          *tail_at<D>(c.tail_v, c, R.row, jc, head, off, ch) = new_val(rel0 + off);
+        for (int i = 0; i < NCH; ++i) {
+          const int off = off0 + i;
+          const bool fresh = off >= lo && off < hi, old = off < lo && pg >= 0;
+          const size_t at = ((size_t)(R.t_begin + (fresh ? rel0 + off : 0)) * c.h_kv + head) * D + ch;
+          const void* ks = old ? (const void*)tail_at<D>(c.tail_k, c, R.row, j, head, off, ch) : (const void*)(k + at);
+          const void* vs = old ? (const void*)tail_at<D>(c.tail_v, c, R.row, j, head, off, ch) : (const void*)(v + at);
+          if (!CONV || !fresh) cp_async16_zfill(dst + i * THREADS, ks, old || fresh);
+          cp_async16_zfill(dst + (NCH + i) * THREADS, vs, old || fresh);
         }
       }
+      cp_async_commit();
+    };
+    fetch(head0);
+    for (int head = head0; head < head1; ++head) {
+      fetch(head + 1);
+      uint4 x[NCH], y[NCH];
+      if constexpr (CONV) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+          if (off0 + i >= lo && off0 + i < hi) x[i] = conv8<D>(c, R, k, w, head, ch, rel0 + off0 + i);
+      }
+      cp_async_wait<1>();
+      const uint4* src = ring + ((head - head0) & 1) * S::STAGE + tid;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        if (!CONV || off0 + i < lo || off0 + i >= hi) x[i] = src[i * THREADS];
+        y[i] = src[(NCH + i) * THREADS];
+      }
+      float mk = finite_amax<NCH>(x, &bad), mv = finite_amax<NCH>(y, &bad);
+      if (keep) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+          if (off0 + i >= lo && off0 + i < hi) {
+            *tail_at<D>(c.tail_k, c, R.row, j, head, off0 + i, ch) = x[i];
+            *tail_at<D>(c.tail_v, c, R.row, j, head, off0 + i, ch) = y[i];
+          }
+      }
+      if (pg < 0) continue;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(~0u, mk, off));
+        mv = fmaxf(mv, __shfl_xor_sync(~0u, mv, off));
+      }
+      if ((tid & 31) == 0) red[0][tid >> 5] = mk, red[1][tid >> 5] = mv;
+      {
+        double s[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = 0.0;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          float f[8];
+          bf16x8_to_f32(x[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] += (double)f[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gsum[(tid / LANES * 8 + e) * LANES + tid % LANES] = s[e];
+      }
+      __syncthreads();
+      mk = red[0][0], mv = red[1][0];
+#pragma unroll
+      for (int i = 1; i < THREADS / 32; ++i) mk = fmaxf(mk, red[0][i]), mv = fmaxf(mv, red[1][i]);
+      const float sk = scale_of<KIND>(mk), sv = scale_of<KIND>(mv);
+      const size_t at = (size_t)pg * c.h_kv + head;
+      write_codes<KIND, D, BLK>(c.k + at * (B * D), x, sk);
+      write_codes<KIND, D, BLK>(c.v + at * (B * D), y, sv);
+      if (tid == 0) c.k_scale[at] = sk, c.v_scale[at] = sv;
+      if (tid < D) {
+        double t = 0.0;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) t += gsum[(g * 8 + (tid & 7)) * LANES + tid / 8];
+        const float mean = (float)(t * (1.0 / B));
+        const bf16 hi16 = __float2bfloat16_rn(mean);
+        c.cent[at * D + tid] = hi16;
+        c.cent[((size_t)c.n_pages * c.h_kv + at) * D + tid] = __float2bfloat16_rn(mean - __bfloat162float(hi16));
+      }
+      __syncthreads();
     }
-    if constexpr (CONV) {
-      __syncthreads();  // the history has been read
-      const int m = min(R.n, Wm1), i = tid / LANES;
-      if (i < m) {
-        const int rel = R.n - m + i;
-        *reinterpret_cast<uint4*>(
-            c.hist + (((size_t)R.row * kHistRing + ((R.pos0 + rel) & (kHistRing - 1))) * c.h_kv + head) * D + ch) =
-            raw_key<D>(c, R, k, head, ch, rel);
+    cp_async_wait<0>();
+  }
+  if (is_first) {
+    int jc = j_last;  // the later one of the last two blocks in the first block's bank
+    if ((jc ^ j_first) & 1) --jc;
+    const bool replace = has_old && jc > j_first;
+    if (replace || CONV) __syncthreads();  // the earlier tokens and the history have been read
+    for (int head = head0; head < head1; ++head) {
+      if (replace) {
+        const int hi = min(R.len - jc * B, B), rel0 = jc * B - R.pos0;
+        for (int off = off0; off < min(off0 + NCH, hi); ++off) {
+          uint4 x;
+          if constexpr (CONV) x = conv8<D>(c, R, k, w, head, ch, rel0 + off);
+          else x = raw_key<D>(c, R, k, head, ch, rel0 + off);
+          const size_t at = ((size_t)(R.t_begin + rel0 + off) * c.h_kv + head) * D + ch;
+          *tail_at<D>(c.tail_k, c, R.row, jc, head, off, ch) = finite8(x, &bad);
+          *tail_at<D>(c.tail_v, c, R.row, jc, head, off, ch) = finite8(__ldg(reinterpret_cast<const uint4*>(v + at)), &bad);
+        }
+      }
+      if constexpr (CONV) {
+        const int m = min(R.n, Wm1), i = tid / LANES;
+        if (i < m) {
+          const int rel = R.n - m + i;
+          *reinterpret_cast<uint4*>(
+              c.hist + (((size_t)R.row * kHistRing + ((R.pos0 + rel) & (kHistRing - 1))) * c.h_kv + head) * D + ch) =
+              raw_key<D>(c, R, k, head, ch, rel);
+        }
       }
     }
   }
   if (bad) set_status(status, kStatusNonFinite);
 }
 
-template <int KIND, int D, int NCH>
+template <int KIND, int D, int BLK>
 cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int32_t* status,
                        cudaStream_t st) {
+  using S = Shape<D, BLK>;
   // Runs of a row start at index cu / B + 2 row at the earliest; with few tokens a row every token stands for its run.
   const long long runs = (long long)p.T / c.B + 2ll * c.rows;
   const int per_token = p.T <= runs;
-  const dim3 grid((unsigned)(per_token ? p.T : runs), c.h_kv);
-  if (c.conv_width > 0) append_kernel<KIND, D, NCH, true><<<grid, kThreads, 0, st>>>(c, p, k, v, w, per_token, status);
-  else append_kernel<KIND, D, NCH, false><<<grid, kThreads, 0, st>>>(c, p, k, v, w, per_token, status);
+  const long long n = per_token ? p.T : runs;
+  // Heads one after the other in a CTA share its look-ups and overlap copies with rounding, as long as the GPU is
+  // filled (8 CTAs per SM).
+  long long per = n * c.h_kv / (8 * 148);
+  per = per < 1 ? 1 : (per > c.h_kv ? c.h_kv : per);
+  const dim3 grid((unsigned)n, (unsigned)((c.h_kv + per - 1) / per));
+  cudaError_t e;
+  if (c.conv_width > 0) {
+    if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  S::BYTES)) != cudaSuccess)
+      return e;
+    append_kernel<KIND, D, BLK, true><<<grid, S::THREADS, S::BYTES, st>>>(c, p, k, v, w, per_token, (int)per, status);
+  } else {
+    if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  S::BYTES)) != cudaSuccess)
+      return e;
+    append_kernel<KIND, D, BLK, false><<<grid, S::THREADS, S::BYTES, st>>>(c, p, k, v, w, per_token, (int)per, status);
+  }
   return cudaGetLastError();
 }
 
 template <int KIND, int D>
 cudaError_t launch_block(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int32_t* status,
                          cudaStream_t st) {
-  switch (c.B * D / 1024) {
-    case 1: if constexpr (D == 64) return launch_one<KIND, D, 1>(c, p, k, v, w, status, st);
-    case 2: return launch_one<KIND, D, 2>(c, p, k, v, w, status, st);
-    case 4: return launch_one<KIND, D, 4>(c, p, k, v, w, status, st);
-    case 8: return launch_one<KIND, D, 8>(c, p, k, v, w, status, st);
-    default: if constexpr (D == 128) return launch_one<KIND, D, 16>(c, p, k, v, w, status, st);
+  switch (c.B) {
+    case 16: return launch_one<KIND, D, 16>(c, p, k, v, w, status, st);
+    case 32: return launch_one<KIND, D, 32>(c, p, k, v, w, status, st);
+    case 64: return launch_one<KIND, D, 64>(c, p, k, v, w, status, st);
+    default: return launch_one<KIND, D, 128>(c, p, k, v, w, status, st);
   }
-  return cudaErrorInvalidValue;
 }
 
 }  // namespace
