@@ -65,6 +65,10 @@ cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, i
 size_t attn_scratch(const View& c, int T, int h_q);
 cudaError_t launch_attention(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk,
                              bf16* out, float* lse, void* scratch, int32_t* status, cudaStream_t st);
+// Attention over all blocks for steps with many tokens per request (cache_attn_rows.cu); `tiles` bounds the tiles of
+// 128 query rows, split_blocks * B is a multiple of 128.
+cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks,
+                                  int nsplit, bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st);
 
 // Where block j of a row is read from: its page (complete blocks), its tail
 // bank, or nowhere (an entry out of range).

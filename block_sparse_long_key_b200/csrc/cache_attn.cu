@@ -673,32 +673,37 @@ merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float*
   if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
 }
 
-struct Split {
-  int blocks;  // per split
-  int n;
+// How a step over all blocks is cut up.
+struct Cut {
+  bool many;       // tiles of 128 rows (cache_attn_rows.cu) instead of 16
+  bool per_token;  // tiles of 16: each token on its own, or a request's tokens together, whichever bound is less
+  long long tiles;
+  int split_blocks, nsplit;
 };
 
-// Long rows are cut into splits of whole blocks, so that even few rows fill
+// Long rows are cut into splits of whole blocks, so that even few tiles fill
 // the GPU: about four CTAs per SM counted over rows of full length, and at
 // least 512 tokens each (a split costs a partial result of D + 4 floats per
 // query row, written and read back).
-Split split_of(const View& c, long long tiles) {
-  const long long ctas = tiles * c.h_kv;
+Cut cut_of(const View& c, int T, int h_q) {
+  const int G = h_q / c.h_kv;
+  const long long a = (long long)T * ((G + 15) / 16), b = (long long)T * G / 16 + c.rows;
+  const long long big = (long long)T * G / 128 + (T < c.rows ? T : c.rows);
+  Cut x;
+  x.per_token = a <= b;
+  x.tiles = x.per_token ? a : b;
+  x.many = x.tiles >= 2 * big;
+  if (x.many) x.tiles = (long long)T * G / 128 + c.rows;
+  const long long ctas = (x.many ? big : x.tiles) * c.h_kv;
   const long long want = (4 * 148 + ctas - 1) / ctas;
+  const long long step = x.many && c.B < 128 ? 128 / c.B : 1;  // splits of whole key tiles
   const long long least = (512 + c.B - 1) / c.B;
   long long blocks = (c.max_blocks + want - 1) / want;
   if (blocks < least) blocks = least;
-  if (blocks > c.max_blocks) blocks = c.max_blocks;
-  return Split{(int)blocks, (int)((c.max_blocks + blocks - 1) / blocks)};
-}
-
-// Tiles of 16 rows of a step's (token, group member) rows, per KV head: each
-// token on its own, or a request's tokens together, whichever bound is less.
-long long tiles_of(const View& c, int T, int h_q, bool* per_token) {
-  const int G = h_q / c.h_kv;
-  const long long a = (long long)T * ((G + 15) / 16), b = (long long)T * G / 16 + c.rows;
-  *per_token = a <= b;
-  return a <= b ? a : b;
+  blocks = (blocks + step - 1) / step * step;
+  x.split_blocks = (int)blocks;
+  x.nsplit = (int)((c.max_blocks + blocks - 1) / blocks);
+  return x;
 }
 
 template <int D, int KIND>
@@ -726,18 +731,21 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
     }
     return cudaGetLastError();
   }
-  bool per_token;
-  const long long tiles = tiles_of(c, p.T, h_q, &per_token);
-  const Split sp = split_of(c, tiles);
-  constexpr int NW = 4;
-  if ((e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Ly::bytes(NW))) != cudaSuccess)
-    return e;
-  attn_kernel<D, KIND, NW, false><<<dim3((unsigned)tiles, c.h_kv, sp.n), NW * 32, Ly::bytes(NW), st>>>(
-      c, p, q, h_q, nullptr, 0, per_token, sp.blocks, sp.n, out, lse, part, status);
-  if ((e = cudaGetLastError()) != cudaSuccess || sp.n == 1) return e;
+  const Cut x = cut_of(c, p.T, h_q);
+  if (x.many) {
+    e = launch_attention_rows(c, p, q, h_q, (int)x.tiles, x.split_blocks, x.nsplit, out, lse, part, status, st);
+    if (e != cudaSuccess || x.nsplit == 1) return e;
+  } else {
+    constexpr int NW = 4;
+    if ((e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  Ly::bytes(NW))) != cudaSuccess)
+      return e;
+    attn_kernel<D, KIND, NW, false><<<dim3((unsigned)x.tiles, c.h_kv, x.nsplit), NW * 32, Ly::bytes(NW), st>>>(
+        c, p, q, h_q, nullptr, 0, x.per_token, x.split_blocks, x.nsplit, out, lse, part, status);
+    if ((e = cudaGetLastError()) != cudaSuccess || x.nsplit == 1) return e;
+  }
   const long long items = (long long)p.T * h_q;
-  merge_kernel<D><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, sp.blocks, sp.n, part, out, lse);
+  merge_kernel<D><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
   return cudaGetLastError();
 }
 
@@ -745,9 +753,8 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
 
 size_t attn_scratch(const View& c, int T, int h_q) {
   if (T == 0) return 0;
-  bool per_token;
-  const Split sp = split_of(c, tiles_of(c, T, h_q, &per_token));
-  return sp.n == 1 ? 0 : (size_t)T * h_q * sp.n * (c.d + 4) * sizeof(float);
+  const Cut x = cut_of(c, T, h_q);
+  return x.nsplit == 1 ? 0 : (size_t)T * h_q * x.nsplit * (c.d + 4) * sizeof(float);
 }
 
 cudaError_t launch_attention(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk,

@@ -1,0 +1,523 @@
+// Attention over the whole cache for many new queries of a request (chunks of
+// a prompt): the arithmetic of cache_attn.cu on tcgen05.
+//
+// A CTA takes 128 query rows ((token, group member) of one request and KV
+// head; row = TMEM lane = softmax thread) and walks key tiles of 128 positions.
+//   producers (4 warps)  8-bit pages -> fp16 K and V tiles in shared memory
+//                        (128-byte swizzle); the partial block's bf16 goes the
+//                        same way under a power of two that keeps every bit
+//   softmax (4 warps)    S from TMEM, weights back into the columns of S as fp16;
+//                        one of their threads issues the products,
+//                        S = Q K^T (M = N = 128, K = d) and O += P V (N = d, K = 128)
+// S and O take 256 TMEM columns and the tiles 96 KB (d = 128), so two CTAs
+// share an SM and one's products run under the other's exponentials.  The
+// reference of a row moves only when its maximum grows by more than 2^8, so O
+// (in TMEM) is seldom rescaled: weights are 2^(x - m + 7) <= 2^15.
+//
+// Both the exponentials (128 x 128 per tile, 16 per clock and SM) and the
+// products (2 x 128 x 128 x d) come to about 1000 clocks per tile and SM at
+// d = 128; the conversion of a tile is 128 threads x 2 d pieces beside them.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "cache.cuh"
+#include "tc.cuh"
+
+namespace moba {
+namespace cache {
+namespace {
+
+constexpr int kRows = 128;      // query rows per CTA
+constexpr int kKeys = 128;      // key positions per tile
+constexpr int kUnits = 8;       // units of 16 positions per tile
+constexpr int kThreads = 256;   // 4 softmax warps, 4 producer warps
+constexpr float kOffset = 7.f;
+constexpr float kSlack = 8.f;   // growth of a row's maximum that leaves its reference alone
+
+template <int D>
+struct Layout {
+  static constexpr int KB = D / 64;
+  static constexpr uint32_t REGION = 128 * 128;  // 128 rows of 64 fp16
+  static constexpr uint32_t Q_OFF = 0, K_OFF = KB * REGION, V_OFF = 2 * KB * REGION;
+  static constexpr uint32_t UNIT_OFF = 3 * KB * REGION;         // float4 [2][8]: ks, lv, rest, 2^-7 / vs
+  static constexpr uint32_t RED_OFF = UNIT_OFF + 2 * kUnits * 16;
+  static constexpr uint32_t MB_OFF = RED_OFF + 64;              // K full, V full, S, P, O
+  static constexpr uint32_t HOLD_OFF = MB_OFF + 40;
+  static constexpr uint32_t FAIL_OFF = HOLD_OFF + 4;
+  static constexpr uint32_t BYTES = FAIL_OFF + 16 + 1024;
+  static constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;
+};
+
+// Instruction descriptor: fp16 operands, fp32 sums.
+constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+template <int KIND>
+__device__ __forceinline__ uint32_t widen2(uint32_t x) {  // low two codes to an fp16 pair
+  if constexpr (KIND == 0) {
+    uint32_t r;
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(x));
+    return r;
+  } else {
+    const uint32_t a = __byte_perm(x ^ 0x8080u, 0x64646464u, 0x4140);  // 0x64bb is 1024 + bb
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// 16 codes to 32 bytes of fp16.
+template <int KIND>
+__device__ __forceinline__ void widen16(uint4 w, uint4& a, uint4& b) {
+  a = make_uint4(widen2<KIND>(w.x), widen2<KIND>(w.x >> 16), widen2<KIND>(w.y), widen2<KIND>(w.y >> 16));
+  b = make_uint4(widen2<KIND>(w.z), widen2<KIND>(w.z >> 16), widen2<KIND>(w.w), widen2<KIND>(w.w >> 16));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// Exponent of a magnitude, within what keeps 2^(14 - e) and 2^(e - 14) normal.
+__device__ __forceinline__ int exponent(float m) { return max(-100, min(127, (int)((__float_as_uint(m) >> 23) & 255) - 127)); }
+
+// 8 bf16 times a power of two, as fp16.
+__device__ __forceinline__ uint4 scale8(uint4 x, float up) {
+  float f[8];
+  bf16x8_to_f32(x, f);
+  return make_uint4(pack_f16(f[0] * up, f[1] * up), pack_f16(f[2] * up, f[3] * up), pack_f16(f[4] * up, f[5] * up),
+                    pack_f16(f[6] * up, f[7] * up));
+}
+
+__device__ __forceinline__ float amax8(uint4 x, float m) {
+  float f[8];
+  bf16x8_to_f32(x, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  return m;
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_blocks, int nsplit,
+                 bf16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int32_t* status) {
+  using Ly = Layout<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  const uint32_t sbase = smem_u32(sm);
+  const uint32_t mb_k = sbase + Ly::MB_OFF, mb_v = mb_k + 8, mb_s = mb_k + 16, mb_p = mb_k + 24, mb_o = mb_k + 32;
+  volatile int* fail = reinterpret_cast<volatile int*>(sm + Ly::FAIL_OFF);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = h_q / c.h_kv, head = blockIdx.y, split = blockIdx.z, u0 = blockIdx.x;
+
+  // ---- the tile's rows
+  int lo = 0, hi = c.rows;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((long long)__ldg(p.cu + mid) * G / kRows + mid <= u0) lo = mid; else hi = mid;
+  }
+  const int row = lo, t0 = __ldg(p.cu + row);
+  const int r0 = (int)(u0 - ((long long)t0 * G / kRows + row)) * kRows;
+  const int nrows = (min(__ldg(p.cu + row + 1), p.T) - t0) * G;
+  if (r0 >= nrows) return;
+  const int rows = min(kRows, nrows - r0);
+  const int len = c.state[2 * row], held = c.state[2 * row + 1];
+  auto pos_of = [&](int r) {
+    const int x = __ldg(p.pos + t0 + (r0 + r) / G);
+    return x < len && x / c.B < held ? x : -1;
+  };
+  // positions ascend along a request's tokens
+  const int mp = pos_of(rows - 1);
+  const int own = mp < 0 ? -1 : mp / c.B;
+  const int b0 = min(own + 1, split * split_blocks), b1 = min(own + 1, b0 + split_blocks);
+  if (split > 0 && b0 >= b1) return;
+  const int kt0 = b0 * c.B / kKeys;                                  // split_blocks * B is a multiple of kKeys
+  const int kend = min(b1 * c.B, mp + 1);                            // first position behind this CTA's keys
+  const int nt = mp < 0 ? 0 : (kend - kt0 * kKeys + kKeys - 1) / kKeys;
+  const int tail0 = (long long)(own + 1) * c.B > len ? own * c.B : 0x7fffffff;  // first position read from the tail
+
+  if (tid == 0) {
+    tc::mbar_init(mb_k, 4);
+    tc::mbar_init(mb_v, 4);
+    tc::mbar_init(mb_s, 1);
+    tc::mbar_init(mb_p, 4);
+    tc::mbar_init(mb_o, 1);
+    tc::mbar_init_fence();
+    *fail = 0;
+  }
+  if (warp == 4) tc::tmem_alloc(sbase + Ly::HOLD_OFF, Ly::TMEM_COLS);
+
+  // ---- queries: fp16 after a power of two per row that brings the largest magnitude to [2^8, 2^9)
+  float fac = 0.f;
+  int pos = -1;
+  size_t item = 0;
+  if (warp < 4) {
+    uint4 x[D / 8];
+    float m = 0.f;
+    if (tid < rows) {
+      pos = pos_of(tid);
+      if (split == 0 && pos != __ldg(p.pos + t0 + (r0 + tid) / G)) set_status(status, kStatusBadTable);
+      item = (size_t)(t0 + (r0 + tid) / G) * h_q + head * G + (r0 + tid) % G;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      x[i] = tid < rows ? __ldg(reinterpret_cast<const uint4*>(q + item * D) + i) : make_uint4(0, 0, 0, 0);
+      m = amax8(x[i], m);
+    }
+    const int e = exponent(m);
+    const float up = pow2f(8 - e);
+    fac = pow2f(e - 8) * (kLog2e * rsqrtf((float)D));
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      *reinterpret_cast<uint4*>(sm + Ly::Q_OFF + (i / 8) * Ly::REGION + tc::sw128_offset(tid, i % 8)) = scale8(x[i], up);
+    tc::fence_proxy_async();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + Ly::HOLD_OFF);
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+  float m = -CUDART_INF_F, l = 0.f;
+
+  if (warp >= 4) {
+    // =============================================================== producers
+    const int pw = warp - 4;
+    int tail_e[2] = {0, 0};
+    if (nt > 0 && kend > tail0) {  // exponents of the tail's largest key and value
+      float am[2] = {0.f, 0.f};
+      const int n = (mp + 1 - tail0) * (D / 8);
+      const size_t at = (((size_t)row * 2 + (own & 1)) * c.h_kv + head) * c.B * D;
+      for (int i = tid - 128; i < n; i += 128) {
+        am[0] = amax8(*(reinterpret_cast<const uint4*>(c.tail_k + at) + i), am[0]);
+        am[1] = amax8(*(reinterpret_cast<const uint4*>(c.tail_v + at) + i), am[1]);
+      }
+      float* red = reinterpret_cast<float*>(sm + Ly::RED_OFF);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int off = 16; off; off >>= 1) am[z] = fmaxf(am[z], __shfl_xor_sync(~0u, am[z], off));
+        if (lane == 0) red[z * 4 + pw] = am[z];
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        tail_e[z] = exponent(fmaxf(fmaxf(red[4 * z], red[4 * z + 1]), fmaxf(red[4 * z + 2], red[4 * z + 3])));
+    }
+    // This warp's units of a tile: 2 pw, 2 pw + 1.  A lane's piece i of a unit is 16 codes (chunk lane + 32 i).
+    constexpr int NP = D / 32;
+    auto unit_pos = [&](int i, int x) { return (kt0 + i) * kKeys + (2 * pw + x) * 16; };
+    auto unit_page = [&](int i, int x) -> int {  // page; -1: zeros; -2: tail
+      const int ps = unit_pos(i, x);
+      if (i >= nt || ps >= kend) return -1;
+      if (ps >= tail0) return -2;
+      const int pg = block_page(c, row, ps / c.B);
+      if (pg < 0) set_status(status, kStatusBadTable);
+      return pg;
+    };
+    // address of a unit's codes inside the pages
+    auto unit_at = [&](int pg, int i, int x) {
+      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) % c.B) * D;
+    };
+    auto put = [&](uint32_t base, int x, int piece, uint4 a, uint4 b) {
+      const int idx = lane + 32 * piece, r = (2 * pw + x) * 16 + idx / (D / 16), ck = idx % (D / 16);
+      unsigned char* dst = sm + base + (ck / 4) * Ly::REGION;
+      *reinterpret_cast<uint4*>(dst + tc::sw128_offset(r, (ck % 4) * 2)) = a;
+      *reinterpret_cast<uint4*>(dst + tc::sw128_offset(r, (ck % 4) * 2 + 1)) = b;
+    };
+    auto put_tail = [&](uint32_t base, const bf16* tail, int i, int x, float up) {
+      const size_t at = (((size_t)row * 2 + (own & 1)) * c.h_kv + head) * c.B * D;
+      const int first = unit_pos(i, x) - tail0, n = mp + 1 - tail0;
+#pragma unroll
+      for (int piece = 0; piece < NP; ++piece) {
+        const int idx = lane + 32 * piece, r = first + idx / (D / 16), ck = idx % (D / 16);
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (r < n) {
+          const uint4* src = reinterpret_cast<const uint4*>(tail + at + (size_t)r * D + ck * 16);
+          a = scale8(src[0], up), b = scale8(src[1], up);
+        }
+        put(base, x, piece, a, b);
+      }
+    };
+    int pg[2] = {unit_page(0, 0), unit_page(0, 1)};
+    for (int i = 0; i < nt; ++i) {
+      uint4 kr[2][NP], vr[2][NP];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint4* ks = reinterpret_cast<const uint4*>(c.k + (pg[x] >= 0 ? unit_at(pg[x], i, x) : 0)) + lane;
+        const uint4* vs = reinterpret_cast<const uint4*>(c.v + (pg[x] >= 0 ? unit_at(pg[x], i, x) : 0)) + lane;
+#pragma unroll
+        for (int z = 0; z < NP; ++z) {
+          kr[x][z] = pg[x] >= 0 ? __ldg(ks + 32 * z) : make_uint4(0, 0, 0, 0);
+          vr[x][z] = pg[x] >= 0 ? __ldg(vs + 32 * z) : make_uint4(0, 0, 0, 0);
+        }
+      }
+      float4 prm = make_float4(0.f, 0.f, 1.f, 0.f);
+      if (lane < 2) {
+        const int g = lane ? pg[1] : pg[0];
+        float ks = 0.f, vs = 1.f;  // nothing here: weights 0
+        if (g >= 0) {
+          const size_t at = (size_t)g * c.h_kv + head;
+          ks = __ldg(c.k_scale + at), vs = __ldg(c.v_scale + at);
+        } else if (g == -2) {
+          ks = pow2f(tail_e[0] - 14), vs = pow2f(tail_e[1] - 14);
+        }
+        const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
+        prm = make_float4(ks, g == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);
+      }
+      const int next[2] = {unit_page(i + 1, 0), unit_page(i + 1, 1)};
+      // K tile free: the products of tile i - 1's scores are done
+      if (!__all_sync(~0u, i == 0 || tc::mbar_wait(mb_s, (i - 1) & 1)) || *fail) { *fail = 1; break; }
+      if (lane < 2) *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + 2 * pw + lane) * 16) = prm;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (pg[x] == -2) {
+          put_tail(Ly::K_OFF, c.tail_k, i, x, pow2f(14 - tail_e[0]));
+        } else {
+#pragma unroll
+          for (int z = 0; z < NP; ++z) {
+            uint4 a, b;
+            widen16<KIND>(kr[x][z], a, b);
+            put(Ly::K_OFF, x, z, a, b);
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(mb_k);
+      // V tile free
+      if (!__all_sync(~0u, i == 0 || tc::mbar_wait(mb_o, (i - 1) & 1)) || *fail) { *fail = 1; break; }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (pg[x] == -2) {
+          put_tail(Ly::V_OFF, c.tail_v, i, x, pow2f(14 - tail_e[1]));
+        } else {
+#pragma unroll
+          for (int z = 0; z < NP; ++z) {
+            uint4 a, b;
+            widen16<KIND>(vr[x][z], a, b);
+            put(Ly::V_OFF, x, z, a, b);
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(mb_v);
+      pg[0] = next[0], pg[1] = next[1];
+    }
+  } else {
+    // =============================================================== softmax
+    constexpr uint32_t id_s = idesc_f16(kRows, kKeys, 0), id_o = idesc_f16(kRows, D, 1);
+    for (int i = 0; i < nt; ++i) {
+      bool got = true;
+      if (tid == 0) {
+        // the weights of the tile before, which these scores overwrite, have been read
+        got = (i == 0 || tc::mbar_wait(mb_o, (i - 1) & 1)) && tc::mbar_wait(mb_k, i & 1);
+        if (got) {
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * Ly::REGION + (kk & 3) * 32;
+            tc::mma_bf16_ss(tmem + Ly::TM_S, tc::smem_desc(sbase + Ly::Q_OFF + o, 16, 1024, tc::kLayoutSW128),
+                            tc::smem_desc(sbase + Ly::K_OFF + o, 16, 1024, tc::kLayoutSW128), id_s, kk > 0);
+          }
+          tc::mma_commit(mb_s);
+        }
+      }
+      __syncwarp();
+      got = got && tc::mbar_wait(mb_s, i & 1);
+      if (!__all_sync(~0u, got) || *fail) { *fail = 1; break; }
+      tc::fence_after_sync();
+      const float4* prm = reinterpret_cast<const float4*>(sm + Ly::UNIT_OFF + (i & 1) * kUnits * 16);
+      const int nvis = min(kKeys, min(pos + 1, kend) - (kt0 + i) * kKeys);  // visible keys of this row, from the first
+      const bool whole = __all_sync(~0u, nvis == kKeys);
+      float top[kUnits];  // largest score of each unit
+#pragma unroll
+      for (int h = 0; h < kKeys / 32; ++h) {
+        uint32_t s[32];
+        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 32, s);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float t = -CUDART_INF_F;
+          if (whole) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (32 * h + 16 * u + x < nvis) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
+          }
+          top[2 * h + u] = t;
+        }
+      }
+      // The units' scales: published with the V tile (whose barrier, unlike the K tile's, cannot get ahead of this warp).
+      if (!__all_sync(~0u, tc::mbar_wait(mb_v, i & 1))) { *fail = 1; break; }
+      float mx = -CUDART_INF_F;
+      bool odd = false;  // a V scale below 2^-100
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const float4 pr = prm[u];
+        if (top[u] > -CUDART_INF_F) mx = fmaxf(mx, fmaf(top[u], fac * pr.x, pr.y));
+        odd |= pr.z != 1.f;
+      }
+      const bool up = mx > m + kSlack;  // m = -infinity: any
+      if (__any_sync(~0u, up)) {
+        const float a = up ? fast_exp2(m - mx) : 1.f;
+        if (up) m = mx;
+        l *= a;
+        if (i > 0) {
+#pragma unroll
+          for (int h = 0; h < D / 32; ++h) {
+            uint32_t o[32];
+            tc::tmem_ld32(tmem + lane_base + Ly::TM_O + h * 32, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
+            tc::tmem_st32(tmem + lane_base + Ly::TM_O + h * 32, o);
+          }
+        }
+      }
+      const float off = kOffset - (m == -CUDART_INF_F ? 0.f : m);
+#pragma unroll
+      for (int hp = 0; hp < 2; ++hp) {
+        uint32_t w[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[32];
+          tc::tmem_ld32(tmem + lane_base + Ly::TM_S + (2 * hp + h) * 32, s);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4 pr = prm[2 * (2 * hp + h) + u];
+            const float f = fac * pr.x, b = pr.y + off;
+            float sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              float e0 = fast_exp2(fmaf(__uint_as_float(s[16 * u + x]), f, b));
+              float e1 = fast_exp2(fmaf(__uint_as_float(s[16 * u + x + 1]), f, b));
+              if (!whole) {
+                const int col = 32 * (2 * hp + h) + 16 * u + x;
+                e0 = col < nvis ? e0 : 0.f;
+                e1 = col + 1 < nvis ? e1 : 0.f;
+              }
+              sum += e0 + e1;
+              if (odd) e0 *= pr.z, e1 *= pr.z;
+              w[16 * h + 8 * u + x / 2] = pack_f16(e0, e1);
+            }
+            l = fmaf(sum, pr.w, l);
+          }
+        }
+        tc::tmem_st32(tmem + lane_base + Ly::TM_S + hp * 32, w);
+      }
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(mb_p);
+      got = true;
+      if (tid == 0) {
+        got = tc::mbar_wait(mb_p, i & 1);
+        if (got) {
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_bf16_ts(tmem + Ly::TM_O, tmem + Ly::TM_S + kk * 8,
+                            tc::smem_desc(sbase + Ly::V_OFF + kk * 2048, Ly::REGION, 1024, tc::kLayoutSW128), id_o,
+                            i > 0 || kk > 0);
+          tc::mma_commit(mb_o);
+        }
+      }
+      if (!__all_sync(~0u, got)) { *fail = 1; break; }
+    }
+    // ---- result
+    bool got = nt == 0 || tc::mbar_wait(mb_o, (nt - 1) & 1);
+    got = __all_sync(~0u, got) && !*fail;
+    if (!got) *fail = 1;
+    tc::fence_after_sync();
+    if (got) {
+      const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
+#pragma unroll
+      for (int h = 0; h < D / 32; ++h) {
+        uint32_t o[32];
+        if (nt > 0) {
+          tc::tmem_ld32(tmem + lane_base + Ly::TM_O + h * 32, o);
+          tc::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0;
+        }
+        if (tid < rows) {
+          if (nsplit == 1) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 8) {
+              uint4 y;
+              uint32_t* yy = &y.x;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                yy[z] = pack_bf16(l == 0.f ? 0.f : __uint_as_float(o[x + 2 * z]) * inv,
+                                  l == 0.f ? 0.f : __uint_as_float(o[x + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + item * D + h * 32 + x) = y;
+            }
+          } else {
+            float* b = part + (item * nsplit + split) * (D + 4);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4)  // in units of cache_attn.cu's weights, 2^15
+              *reinterpret_cast<float4*>(b + h * 32 + x) =
+                  make_float4(__uint_as_float(o[x]) * 256.f, __uint_as_float(o[x + 1]) * 256.f,
+                              __uint_as_float(o[x + 2]) * 256.f, __uint_as_float(o[x + 3]) * 256.f);
+          }
+        }
+      }
+      if (tid < rows) {
+        if (nsplit == 1) {
+          lse[item] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          float* b = part + (item * nsplit + split) * (D + 4);
+          b[D] = m, b[D + 1] = l;
+        }
+      }
+    }
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  if (*fail) {
+    // A completion never arrived: record it and give what is in flight a bounded chance to drain.
+    if (tid == 0) set_status(status, kStatusTimeout);
+    tc::mbar_wait(mb_s, 0, 50000000ull);
+    tc::mbar_wait(mb_s, 1, 50000000ull);
+    tc::mbar_wait(mb_o, 0, 50000000ull);
+    tc::mbar_wait(mb_o, 1, 50000000ull);
+    __syncthreads();
+  }
+  if (warp == 4) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, Ly::TMEM_COLS);
+  }
+}
+
+template <int D, int KIND>
+cudaError_t launch(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks, int nsplit,
+                   bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
+  constexpr int smem = Layout<D>::BYTES;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_rows_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_rows_kernel<D, KIND><<<dim3(tiles, c.h_kv, nsplit), kThreads, smem, st>>>(c, p, q, h_q, split_blocks, nsplit, out,
+                                                                               lse, part, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks,
+                                  int nsplit, bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
+  if (c.d == 64)
+    return c.kind == 0 ? launch<64, 0>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
+                       : launch<64, 1>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
+  return c.kind == 0 ? launch<128, 0>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
+                     : launch<128, 1>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
+}
+
+}  // namespace cache
+}  // namespace moba

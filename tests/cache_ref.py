@@ -136,13 +136,14 @@ class RefCache:
         return sel
 
     def attend(self, row, pos, q, sel=None):
-        """out, lse, and the two bounds' parts: sum p|v| and the score error scale, all float64."""
+        """out, lse, and the bounds' parts: sum p|v|, the score error scale, keys x largest |v|; all float64."""
         T, hq, d = q.shape
         g = hq // self.h
         out = torch.zeros((T, hq, d), dtype=torch.float64)
         lse = torch.full((T, hq), -math.inf, dtype=torch.float64)
         mass = torch.zeros((T, hq, d), dtype=torch.float64)
         size = torch.zeros((T, hq), dtype=torch.float64)
+        low = torch.zeros((T, hq), dtype=torch.float64)
         held = {}
         for t in range(T):
             if row[t] < 0 or pos[t] < 0:
@@ -164,18 +165,24 @@ class RefCache:
                 mass[t, h] = (p[:, None] * v.abs()).sum(0)
                 lse[t, h] = torch.logsumexp(s, 0)
                 size[t, h] = (k.abs() * q[t, h].double().abs()).sum(-1).max() / math.sqrt(d)
-        return out, lse, mass, size
+                low[t, h] = len(at) * v.abs().max()
+        return out, lse, mass, size, low
 
 
 def check_attention(out, lse, ref, d, what=""):
     """Output against the reference.  The output is rounded to bf16 once (half a step, 2^-8 of the value).  A weight
     p = exp(s - m) is off by its rounding to fp16 (2^-11), the scores by the rounding of d products and sums and of
     the few steps to the exponent in 32 bits: delta = (d + 16) 2^-24 sum|q k| / sqrt(d); p by about delta + 2^-20
-    (the exponential).  Both the weights and their sum carry that, hence twice."""
-    o, l, mass, size = ref
+    (the exponential).  Both the weights and their sum carry that, hence twice.
+
+    fp16 also has a smallest step, 2^-24, so a weight is off by up to 2^-25 however small it is.  Weights carry the
+    block's V scale and the largest one is at least 2^7, so with w_i = p_i vs_i c, c >= 2^7 / max(p vs), that moves the
+    output by at most sum_i 2^-25 |v8_i| / c <= 2^-32 sum_i |v8_i| max(p vs) <= 2^-32 n max|v|: |v8_i| is at most the
+    largest code, and that times the largest scale is max|v|."""
+    o, l, mass, size, low = ref
     delta = (d + 16) * 2.0 ** -24 * size + 2.0 ** -20
     err = (out.double() - o).abs()
-    tol = 2.0 ** -8 * o.abs() + (1 + 2.0 ** -7) * mass * (2.0 ** -11 + 2 * torch.expm1(2 * delta))[..., None] + 1e-38
+    tol = 2.0 ** -8 * o.abs() + (1 + 2.0 ** -7) * mass * (2.0 ** -11 + 2 * torch.expm1(2 * delta))[..., None] + 2.0 ** -32 * low[..., None] + 1e-38
     assert torch.isfinite(out.double()).all(), what
     assert (err <= tol).all(), (what, float((err / tol).max()))
     empty = torch.isinf(l)

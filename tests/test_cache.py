@@ -244,3 +244,16 @@ def test_serving_run(shape):
     r.step([4 * B + 2, 9, 17, 2, 1], pad=1)
     for _ in range(3):
         r.step([1, 1, 1, 1, 1])
+
+
+@gpu
+@pytest.mark.parametrize("hq,h,d,B,kind,n,scale", [
+    (4, 1, 128, 64, "e4m3", (300, 129, 1), 1.0),      # several key tiles, rows ending inside one
+    (3, 1, 64, 16, "int8", (257, 40, 128), 4.0),      # sharp softmax: references move
+    (16, 2, 64, 128, "e4m3", (127, 128, 2), 0.05),    # whole and all-but-whole key tiles, flat softmax
+    (2, 2, 128, 32, "int8", (513, 64, 64), 30.0),     # one key takes all
+], ids=str)
+def test_chunks_of_many_tokens(hq, h, d, B, kind, n, scale):
+    r = Run(2, 1400 // B + 4, 1100 // B + 8, hq, h, d, B, kind, 0, 4, seed=B + hq, scale=scale)
+    for a in n:
+        r.step([a, a // 2 + 1])
