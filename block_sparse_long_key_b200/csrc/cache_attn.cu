@@ -695,7 +695,7 @@ Cut cut_of(const View& c, int T, int h_q) {
   x.many = x.tiles >= 2 * big;
   if (x.many) x.tiles = (long long)T * G / 128 + c.rows;
   const long long ctas = (x.many ? big : x.tiles) * c.h_kv;
-  const long long want = (4 * 148 + ctas - 1) / ctas;
+  const long long want = ((x.many ? 6 : 4) * 148 + ctas - 1) / ctas;
   const long long step = x.many && c.B < 128 ? 128 / c.B : 1;  // splits of whole key tiles
   const long long least = (512 + c.B - 1) / c.B;
   long long blocks = (c.max_blocks + want - 1) / want;

@@ -54,24 +54,70 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Four codes to two fp16 pairs, exactly.
 template <int KIND>
-__device__ __forceinline__ uint32_t widen2(uint32_t x) {  // low two codes to an fp16 pair
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {
   if constexpr (KIND == 0) {
-    uint32_t r;
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(x));
-    return r;
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
   } else {
-    const uint32_t a = __byte_perm(x ^ 0x8080u, 0x64646464u, 0x4140);  // 0x64bb is 1024 + bb
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), __half2half2(__ushort_as_half(0x6480)));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    x ^= 0x80808080u;  // 0x64bb is 1024 + bb; with bb = x + 128 subtract 1152
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&ra);
+    hi = *reinterpret_cast<const uint32_t*>(&rb);
   }
 }
 
 // 16 codes to 32 bytes of fp16.
 template <int KIND>
 __device__ __forceinline__ void widen16(uint4 w, uint4& a, uint4& b) {
-  a = make_uint4(widen2<KIND>(w.x), widen2<KIND>(w.x >> 16), widen2<KIND>(w.y), widen2<KIND>(w.y >> 16));
-  b = make_uint4(widen2<KIND>(w.z), widen2<KIND>(w.z >> 16), widen2<KIND>(w.w), widen2<KIND>(w.w >> 16));
+  widen4<KIND>(w.x, a.x, a.y);
+  widen4<KIND>(w.y, a.z, a.w);
+  widen4<KIND>(w.z, b.x, b.y);
+  widen4<KIND>(w.w, b.z, b.w);
+}
+
+// Bounded wait for phase `parity`: the clock is looked at once in 1024 tries.
+__device__ __forceinline__ bool wait(uint32_t addr, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done) : "r"(addr), "r"(parity) : "memory");
+    if (done) return true;
+    if ((n & 1023u) == 0) {
+      const uint64_t now = tc::globaltimer();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > limit_ns) return false;
+    }
+  }
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -205,8 +251,12 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       for (int z = 0; z < 2; ++z)
         tail_e[z] = exponent(fmaxf(fmaxf(red[4 * z], red[4 * z + 1]), fmaxf(red[4 * z + 2], red[4 * z + 3])));
     }
-    // This warp's units of a tile: 2 pw, 2 pw + 1.  A lane's piece i of a unit is 16 codes (chunk lane + 32 i).
+    // This warp's units of a tile: 2 pw, 2 pw + 1.  Piece z of a unit: 16 codes a lane, of row 8 (z / KB) + lane / 4 and
+    // the channels 64 (z % KB) + 16 (lane % 4) on; 8 lanes then store two rows' 64 bytes, every bank once.
     constexpr int NP = D / 32;
+    const int rr = lane >> 2, cq = lane & 3;
+    const uint32_t code_at = rr * D + cq * 16;
+    const uint32_t put_a = rr * 128 + ((2 * cq ^ rr) << 4), put_b = rr * 128 + (((2 * cq + 1) ^ rr) << 4);
     auto unit_pos = [&](int i, int x) { return (kt0 + i) * kKeys + (2 * pw + x) * 16; };
     auto unit_page = [&](int i, int x) -> int {  // page; -1: zeros; -2: tail
       const int ps = unit_pos(i, x);
@@ -218,26 +268,25 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     };
     // address of a unit's codes inside the pages
     auto unit_at = [&](int pg, int i, int x) {
-      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) % c.B) * D;
+      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) % c.B) * D + code_at;
     };
-    auto put = [&](uint32_t base, int x, int piece, uint4 a, uint4 b) {
-      const int idx = lane + 32 * piece, r = (2 * pw + x) * 16 + idx / (D / 16), ck = idx % (D / 16);
-      unsigned char* dst = sm + base + (ck / 4) * Ly::REGION;
-      *reinterpret_cast<uint4*>(dst + tc::sw128_offset(r, (ck % 4) * 2)) = a;
-      *reinterpret_cast<uint4*>(dst + tc::sw128_offset(r, (ck % 4) * 2 + 1)) = b;
+    auto put = [&](uint32_t base, int x, int z, uint4 a, uint4 b) {
+      unsigned char* dst = sm + base + (z % Ly::KB) * Ly::REGION + (2 * (2 * pw + x) + z / Ly::KB) * 1024;
+      *reinterpret_cast<uint4*>(dst + put_a) = a;
+      *reinterpret_cast<uint4*>(dst + put_b) = b;
     };
     auto put_tail = [&](uint32_t base, const bf16* tail, int i, int x, float up) {
       const size_t at = (((size_t)row * 2 + (own & 1)) * c.h_kv + head) * c.B * D;
       const int first = unit_pos(i, x) - tail0, n = mp + 1 - tail0;
-#pragma unroll
-      for (int piece = 0; piece < NP; ++piece) {
-        const int idx = lane + 32 * piece, r = first + idx / (D / 16), ck = idx % (D / 16);
+#pragma unroll 1
+      for (int z = 0; z < NP; ++z) {
+        const int r = first + 8 * (z / Ly::KB) + rr;
         uint4 a = make_uint4(0, 0, 0, 0), b = a;
         if (r < n) {
-          const uint4* src = reinterpret_cast<const uint4*>(tail + at + (size_t)r * D + ck * 16);
+          const uint4* src = reinterpret_cast<const uint4*>(tail + at + (size_t)r * D + 64 * (z % Ly::KB) + 16 * cq);
           a = scale8(src[0], up), b = scale8(src[1], up);
         }
-        put(base, x, piece, a, b);
+        put(base, x, z, a, b);
       }
     };
     int pg[2] = {unit_page(0, 0), unit_page(0, 1)};
@@ -245,12 +294,15 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       uint4 kr[2][NP], vr[2][NP];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint4* ks = reinterpret_cast<const uint4*>(c.k + (pg[x] >= 0 ? unit_at(pg[x], i, x) : 0)) + lane;
-        const uint4* vs = reinterpret_cast<const uint4*>(c.v + (pg[x] >= 0 ? unit_at(pg[x], i, x) : 0)) + lane;
+        const size_t at = pg[x] >= 0 ? unit_at(pg[x], i, x) : 0;
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
-          kr[x][z] = pg[x] >= 0 ? __ldg(ks + 32 * z) : make_uint4(0, 0, 0, 0);
-          vr[x][z] = pg[x] >= 0 ? __ldg(vs + 32 * z) : make_uint4(0, 0, 0, 0);
+          const size_t o = at + (z / Ly::KB) * 8 * D + (z % Ly::KB) * 64;
+          kr[x][z] = vr[x][z] = make_uint4(0, 0, 0, 0);
+          if (pg[x] >= 0) {
+            kr[x][z] = __ldg(reinterpret_cast<const uint4*>(c.k + o));
+            vr[x][z] = __ldg(reinterpret_cast<const uint4*>(c.v + o));
+          }
         }
       }
       float4 prm = make_float4(0.f, 0.f, 1.f, 0.f);
@@ -268,7 +320,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       }
       const int next[2] = {unit_page(i + 1, 0), unit_page(i + 1, 1)};
       // K tile free: the products of tile i - 1's scores are done
-      if (!__all_sync(~0u, i == 0 || tc::mbar_wait(mb_s, (i - 1) & 1)) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, i == 0 || wait(mb_s, (i - 1) & 1)) || *fail) { *fail = 1; break; }
       if (lane < 2) *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + 2 * pw + lane) * 16) = prm;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -287,7 +339,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(mb_k);
       // V tile free
-      if (!__all_sync(~0u, i == 0 || tc::mbar_wait(mb_o, (i - 1) & 1)) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, i == 0 || wait(mb_o, (i - 1) & 1)) || *fail) { *fail = 1; break; }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (pg[x] == -2) {
@@ -313,7 +365,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       bool got = true;
       if (tid == 0) {
         // the weights of the tile before, which these scores overwrite, have been read
-        got = (i == 0 || tc::mbar_wait(mb_o, (i - 1) & 1)) && tc::mbar_wait(mb_k, i & 1);
+        got = (i == 0 || wait(mb_o, (i - 1) & 1)) && wait(mb_k, i & 1);
         if (got) {
           tc::fence_after_sync();
 #pragma unroll
@@ -326,12 +378,24 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         }
       }
       __syncwarp();
-      got = got && tc::mbar_wait(mb_s, i & 1);
+      got = got && wait(mb_s, i & 1);
       if (!__all_sync(~0u, got) || *fail) { *fail = 1; break; }
       tc::fence_after_sync();
       const float4* prm = reinterpret_cast<const float4*>(sm + Ly::UNIT_OFF + (i & 1) * kUnits * 16);
       const int nvis = min(kKeys, min(pos + 1, kend) - (kt0 + i) * kKeys);  // visible keys of this row, from the first
-      const bool whole = __all_sync(~0u, nvis == kKeys);
+      if (!__all_sync(~0u, nvis == kKeys)) {  // hidden scores become -infinity where they are
+#pragma unroll 1
+        for (int h = 0; h < kKeys / 32; ++h) {
+          uint32_t s[32];
+          tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 32, s);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (32 * h + x >= nvis) s[x] = 0xff800000u;
+          tc::tmem_st32(tmem + lane_base + Ly::TM_S + h * 32, s);
+        }
+        tc::tmem_st_wait();
+      }
       float top[kUnits];  // largest score of each unit
 #pragma unroll
       for (int h = 0; h < kKeys / 32; ++h) {
@@ -340,26 +404,21 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         tc::tmem_ld_wait();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float t = -CUDART_INF_F;
-          if (whole) {
+          float t = __uint_as_float(s[16 * u]);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (32 * h + 16 * u + x < nvis) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
-          }
+          for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
           top[2 * h + u] = t;
         }
       }
       // The units' scales: published with the V tile (whose barrier, unlike the K tile's, cannot get ahead of this warp).
-      if (!__all_sync(~0u, tc::mbar_wait(mb_v, i & 1))) { *fail = 1; break; }
+      if (!__all_sync(~0u, wait(mb_v, i & 1))) { *fail = 1; break; }
       float mx = -CUDART_INF_F;
       bool odd = false;  // a V scale below 2^-100
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const float4 pr = prm[u];
-        if (top[u] > -CUDART_INF_F) mx = fmaxf(mx, fmaf(top[u], fac * pr.x, pr.y));
+        // at least 2^-120, so that -infinity stays itself; smaller factors meet scores that they make zero anyway
+        mx = fmaxf(mx, fmaf(top[u], fmaxf(fac * pr.x, 7.5231639e-37f), pr.y));
         odd |= pr.z != 1.f;
       }
       const bool up = mx > m + kSlack;  // m = -infinity: any
@@ -368,7 +427,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         if (up) m = mx;
         l *= a;
         if (i > 0) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < D / 32; ++h) {
             uint32_t o[32];
             tc::tmem_ld32(tmem + lane_base + Ly::TM_O + h * 32, o);
@@ -391,22 +450,28 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const float4 pr = prm[2 * (2 * hp + h) + u];
-            const float f = fac * pr.x, b = pr.y + off;
-            float sum = 0.f;
+            const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f), b1 = pr.y + off;
+            const uint64_t f = pair(f1, f1), b = pair(b1, b1);
+            uint64_t sum = 0;  // two zeros
 #pragma unroll
             for (int x = 0; x < 16; x += 2) {
-              float e0 = fast_exp2(fmaf(__uint_as_float(s[16 * u + x]), f, b));
-              float e1 = fast_exp2(fmaf(__uint_as_float(s[16 * u + x + 1]), f, b));
-              if (!whole) {
-                const int col = 32 * (2 * hp + h) + 16 * u + x;
-                e0 = col < nvis ? e0 : 0.f;
-                e1 = col + 1 < nvis ? e1 : 0.f;
-              }
-              sum += e0 + e1;
-              if (odd) e0 *= pr.z, e1 *= pr.z;
+              float e0, e1;
+              unpair(fma2(pair(__uint_as_float(s[16 * u + x]), __uint_as_float(s[16 * u + x + 1])), f, b), e0, e1);
+              e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+              sum = add2(sum, pair(e0, e1));
               w[16 * h + 8 * u + x / 2] = pack_f16(e0, e1);
             }
-            l = fmaf(sum, pr.w, l);
+            float s0, s1;
+            unpair(sum, s0, s1);
+            l = fmaf(s0 + s1, pr.w, l);
+            if (odd) {
+              const __half2 z = __float2half2_rn(pr.z);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[16 * h + 8 * u + x]), z);
+                w[16 * h + 8 * u + x] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+            }
           }
         }
         tc::tmem_st32(tmem + lane_base + Ly::TM_S + hp * 32, w);
@@ -417,7 +482,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       if (lane == 0) tc::mbar_arrive(mb_p);
       got = true;
       if (tid == 0) {
-        got = tc::mbar_wait(mb_p, i & 1);
+        got = wait(mb_p, i & 1);
         if (got) {
           tc::fence_after_sync();
 #pragma unroll
@@ -431,7 +496,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       if (!__all_sync(~0u, got)) { *fail = 1; break; }
     }
     // ---- result
-    bool got = nt == 0 || tc::mbar_wait(mb_o, (nt - 1) & 1);
+    bool got = nt == 0 || wait(mb_o, (nt - 1) & 1);
     got = __all_sync(~0u, got) && !*fail;
     if (!got) *fail = 1;
     tc::fence_after_sync();
@@ -484,10 +549,10 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   if (*fail) {
     // A completion never arrived: record it and give what is in flight a bounded chance to drain.
     if (tid == 0) set_status(status, kStatusTimeout);
-    tc::mbar_wait(mb_s, 0, 50000000ull);
-    tc::mbar_wait(mb_s, 1, 50000000ull);
-    tc::mbar_wait(mb_o, 0, 50000000ull);
-    tc::mbar_wait(mb_o, 1, 50000000ull);
+    wait(mb_s, 0, 50000000ull);
+    wait(mb_s, 1, 50000000ull);
+    wait(mb_o, 0, 50000000ull);
+    wait(mb_o, 1, 50000000ull);
     __syncthreads();
   }
   if (warp == 4) {
