@@ -258,13 +258,18 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     const uint32_t code_at = rr * D + cq * 16;
     const uint32_t put_a = rr * 128 + ((2 * cq ^ rr) << 4), put_b = rr * 128 + (((2 * cq + 1) ^ rr) << 4);
     auto unit_pos = [&](int i, int x) { return (kt0 + i) * kKeys + (2 * pw + x) * 16; };
-    auto unit_page = [&](int i, int x) -> int {  // page; -1: zeros; -2: tail
+    // A unit's table entry (only loaded here: nothing waits for it), and what it says: page; -1: zeros; -2: tail.
+    auto unit_entry = [&](int i, int x) {
+      const int ps = unit_pos(i, x);
+      return i < nt && ps < kend && ps < tail0 ? __ldg(c.table + (size_t)row * c.max_blocks + ps / c.B) : 0;
+    };
+    auto unit_page = [&](int entry, int i, int x) {
       const int ps = unit_pos(i, x);
       if (i >= nt || ps >= kend) return -1;
       if (ps >= tail0) return -2;
-      const int pg = block_page(c, row, ps / c.B);
-      if (pg < 0) set_status(status, kStatusBadTable);
-      return pg;
+      if ((unsigned)entry < (unsigned)c.n_pages) return entry;
+      set_status(status, kStatusBadTable);
+      return -1;
     };
     // address of a unit's codes inside the pages
     auto unit_at = [&](int pg, int i, int x) {
@@ -289,39 +294,43 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         put(base, x, z, a, b);
       }
     };
-    int pg[2] = {unit_page(0, 0), unit_page(0, 1)};
-    for (int i = 0; i < nt; ++i) {
-      uint4 kr[2][NP], vr[2][NP];
+    // Registers hold one tile's pieces; a tile's are asked for as soon as the ones before have been stored.
+    uint4 kr[2][NP], vr[2][NP];
+    float sc[2] = {0.f, 1.f};  // lanes 0, 1: this lane's unit's scales
+    auto ask = [&](uint4 (*r)[NP], const uint8_t* base, const int* pg, int i) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const size_t at = pg[x] >= 0 ? unit_at(pg[x], i, x) : 0;
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
-          const size_t o = at + (z / Ly::KB) * 8 * D + (z % Ly::KB) * 64;
-          kr[x][z] = vr[x][z] = make_uint4(0, 0, 0, 0);
-          if (pg[x] >= 0) {
-            kr[x][z] = __ldg(reinterpret_cast<const uint4*>(c.k + o));
-            vr[x][z] = __ldg(reinterpret_cast<const uint4*>(c.v + o));
-          }
+          r[x][z] = make_uint4(0, 0, 0, 0);
+          if (pg[x] >= 0) r[x][z] = __ldg(reinterpret_cast<const uint4*>(base + at + (z / Ly::KB) * 8 * D + (z % Ly::KB) * 64));
         }
       }
-      float4 prm = make_float4(0.f, 0.f, 1.f, 0.f);
-      if (lane < 2) {
-        const int g = lane ? pg[1] : pg[0];
-        float ks = 0.f, vs = 1.f;  // nothing here: weights 0
-        if (g >= 0) {
-          const size_t at = (size_t)g * c.h_kv + head;
-          ks = __ldg(c.k_scale + at), vs = __ldg(c.v_scale + at);
-        } else if (g == -2) {
-          ks = pow2f(tail_e[0] - 14), vs = pow2f(tail_e[1] - 14);
-        }
-        const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
-        prm = make_float4(ks, g == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);
+    };
+    auto ask_scales = [&](const int* pg) {
+      const int g = lane ? pg[1] : pg[0];
+      if (lane < 2 && g >= 0) {
+        const size_t at = (size_t)g * c.h_kv + head;
+        sc[0] = __ldg(c.k_scale + at), sc[1] = __ldg(c.v_scale + at);
       }
-      const int next[2] = {unit_page(i + 1, 0), unit_page(i + 1, 1)};
+    };
+    int pg[2] = {unit_page(unit_entry(0, 0), 0, 0), unit_page(unit_entry(0, 1), 0, 1)};
+    int next[2] = {unit_entry(1, 0), unit_entry(1, 1)};
+    ask(kr, c.k, pg, 0);
+    ask(vr, c.v, pg, 0);
+    ask_scales(pg);
+    for (int i = 0; i < nt; ++i) {
       // K tile free: the products of tile i - 1's scores are done
       if (!__all_sync(~0u, i == 0 || wait(mb_s, (i - 1) & 1)) || *fail) { *fail = 1; break; }
-      if (lane < 2) *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + 2 * pw + lane) * 16) = prm;
+      if (lane < 2) {
+        const int g = lane ? pg[1] : pg[0];
+        const float ks = g >= 0 ? sc[0] : (g == -2 ? pow2f(tail_e[0] - 14) : 0.f);
+        const float vs = g >= 0 ? sc[1] : (g == -2 ? pow2f(tail_e[1] - 14) : 1.f);
+        const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
+        *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + 2 * pw + lane) * 16) =
+            make_float4(ks, g == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);  // nothing: weights 0
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (pg[x] == -2) {
@@ -338,6 +347,10 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(mb_k);
+      const int ng[2] = {unit_page(next[0], i + 1, 0), unit_page(next[1], i + 1, 1)};
+      next[0] = unit_entry(i + 2, 0), next[1] = unit_entry(i + 2, 1);
+      ask(kr, c.k, ng, i + 1);
+      ask_scales(ng);
       // V tile free
       if (!__all_sync(~0u, i == 0 || wait(mb_o, (i - 1) & 1)) || *fail) { *fail = 1; break; }
 #pragma unroll
@@ -356,7 +369,8 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(mb_v);
-      pg[0] = next[0], pg[1] = next[1];
+      pg[0] = ng[0], pg[1] = ng[1];
+      ask(vr, c.v, pg, i + 1);
     }
   } else {
     // =============================================================== softmax
@@ -398,16 +412,17 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       }
       float top[kUnits];  // largest score of each unit
 #pragma unroll
-      for (int h = 0; h < kKeys / 32; ++h) {
-        uint32_t s[32];
-        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 32, s);
+      for (int h = 0; h < kKeys / 64; ++h) {
+        uint32_t s[2][32];
+        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 64, s[0]);
+        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 64 + 32, s[1]);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float t = __uint_as_float(s[16 * u]);
+        for (int u = 0; u < 4; ++u) {
+          float t = __uint_as_float(s[u / 2][16 * (u & 1)]);
 #pragma unroll
-          for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[16 * u + x]));
-          top[2 * h + u] = t;
+          for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[u / 2][16 * (u & 1) + x]));
+          top[4 * h + u] = t;
         }
       }
       // The units' scales: published with the V tile (whose barrier, unlike the K tile's, cannot get ahead of this warp).
