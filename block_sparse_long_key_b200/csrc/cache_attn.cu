@@ -20,13 +20,14 @@
 // as hi + lo.
 //
 // Fragments (mma.m16n8k16; lane = 4 g + t).  Keys come 16 tokens (a unit) at a
-// time.  Scores: A = queries, B = keys; column n of n-tile i is the unit's
-// token 4 (n / 2) + 2 i + n % 2, and the k index runs over channels such that a
-// lane's share of a key row is 16 contiguous bytes.  Then a lane's weights are
-// those of tokens 4 t .. 4 t + 3, already in the layout of the A operand of
-// the product with V, and its share of V is 4 token rows of D / 8 contiguous
-// channels, transposed 4 x 4 bytes in registers; column n of output n-tile i
-// is channel (D / 8) n + i.
+// time and are the M side of both products, so that up to 8 query rows (the
+// heads of a group) fill the N side: scores^T = K q^T, out^T = V^T w^T.  Row r
+// of the scores is the unit's token 4 (r / 2) + r % 2 (r < 8; + 2 for r + 8),
+// and the k index runs over channels such that a lane's share of a key row is
+// 16 contiguous bytes.  Transposed in place (movmatrix), a lane's weights are
+// those of tokens 4 t .. 4 t + 3; its share of V is those 4 token rows of D / 8
+// contiguous channels, transposed 4 x 4 bytes in registers, and row r of
+// output tile i is channel (D / 8) (r % 8) + 2 i + r / 8.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
@@ -39,7 +40,7 @@ namespace {
 constexpr int kUnit = 16;        // tokens per unit
 constexpr int kPair = 2;         // units per softmax step
 constexpr float kOffset = 15.f;  // exponent of the largest weight
-constexpr int kListCap = 256;    // list entries held in shared memory at a time
+constexpr int kListCap = 128;    // list entries held in shared memory at a time
 
 // ---------------------------------------------------------------- fragments
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -109,31 +110,40 @@ __device__ __forceinline__ void fetch_unit(unsigned char* dst, const uint8_t* kp
   }
 }
 
-// Scores of one unit: s[i][*] of n-tile i.  qf: D / 16 fragments of the queries.
-template <int D, int KIND>
-__device__ __forceinline__ void unit_scores(const unsigned char* kt, const uint32_t (*qf)[4], float (*s)[4], int g, int t) {
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Scores of one unit for 8 NT query rows: s[n][0, 1] of token 4 (g / 2) + g % 2 and rows 8 n + 2 t, + 1; s[n][2, 3] of
+// the token 2 behind.  qf[n][k]: the queries' fragments.
+template <int D, int KIND, int NT>
+__device__ __forceinline__ void unit_scores(const unsigned char* kt, const uint32_t (*qf)[D / 16][2], float (*s)[4], int g, int t) {
+  const int r = (g >> 1) * 4 + (g & 1);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (g >> 1) * 4 + 2 * i + (g & 1);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
+    for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
 #pragma unroll
-    for (int hh = 0; hh < D / 64; ++hh) {
-      const uint4 w = *reinterpret_cast<const uint4*>(kt + k_place<D>(r, 4 * hh + t));
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  for (int hh = 0; hh < D / 64; ++hh) {
+    const uint4 u = *reinterpret_cast<const uint4*>(kt + k_place<D>(r, 4 * hh + t));
+    const uint4 v = *reinterpret_cast<const uint4*>(kt + k_place<D>(r + 2, 4 * hh + t));
+    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t b0, b1;
-        widen<KIND>(ws[x], b0, b1);
-        mma_f16(s[i], qf[hh * 4 + x], b0, b1);
-      }
+    for (int x = 0; x < 4; ++x) {
+      uint32_t a[4];
+      widen<KIND>(us[x], a[0], a[2]);
+      widen<KIND>(vs[x], a[1], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(s[n], a, qf[n][hh * 4 + x][0], qf[n][hh * 4 + x][1]);
     }
   }
 }
 
-// o += weights (A fragment pf) times the unit's V.
-template <int D, int KIND>
-__device__ __forceinline__ void unit_values(const unsigned char* vt, const uint32_t* pf, float (*o)[4], int g, int t) {
+// o += the unit's V times weights (B fragments pf).
+template <int D, int KIND, int NT>
+__device__ __forceinline__ void unit_values(const unsigned char* vt, const uint32_t (*pf)[2], float (*o)[D / 16][4], int g, int t) {
   constexpr int NW = D / 32;  // words of 4 channels per lane and token
   uint32_t x[4][NW];
 #pragma unroll
@@ -153,55 +163,66 @@ __device__ __forceinline__ void unit_values(const unsigned char* vt, const uint3
     uint32_t y[4];
     transpose4(in, y);
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-      uint32_t b0, b1;
-      widen<KIND>(y[ch], b0, b1);
-      mma_f16(o[4 * w + ch], pf, b0, b1);
+    for (int c2 = 0; c2 < 2; ++c2) {
+      uint32_t a[4];
+      widen<KIND>(y[2 * c2], a[0], a[2]);
+      widen<KIND>(y[2 * c2 + 1], a[1], a[3]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + c2], a, pf[n][0], pf[n][1]);
     }
   }
 }
 
-// Running softmax state of a warp's 16 rows (this lane: rows g and g + 8).
-template <int D>
+// Running softmax state of a warp's 8 NT rows (this lane: rows 8 n + 2 t + b).
+template <int D, int NT>
 struct State {
-  float m[2], l[2];
-  float o[D / 8][4];
+  float m[NT][2], l[NT][2];
+  float o[NT][D / 16][4];
   __device__ __forceinline__ void clear() {
-    m[0] = m[1] = -CUDART_INF_F;
-    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -CUDART_INF_F;
+      l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
+    }
   }
-  // Raises the reference to cover `mx` (this lane's maxima over its columns).
-  __device__ __forceinline__ void raise(float mx0, float mx1) {
-    float mx[2] = {mx0, mx1};
+  // Raises the references to cover mx (this lane's maxima over its tokens).
+  __device__ __forceinline__ void raise(float (*mx)[2]) {
     bool up = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
-      mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
-      up |= mx[r] > m[r];
-    }
-    if (__any_sync(~0u, up)) {
-      float a[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float n = fmaxf(m[r], mx[r]);
-        a[r] = n > m[r] ? fast_exp2(m[r] - n) : 1.f;  // m = -inf: 0
-        m[r] = n;
-        l[r] *= a[r];
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx[n][b] = fmaxf(mx[n][b], __shfl_xor_sync(~0u, mx[n][b], off));
+        up |= mx[n][b] > m[n][b];
       }
+    if (__any_sync(~0u, up)) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= a[0], o[i][1] *= a[0];
-        o[i][2] *= a[1], o[i][3] *= a[1];
+      for (int n = 0; n < NT; ++n) {
+        float a[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float x = fmaxf(m[n][b], mx[n][b]);
+          a[b] = x > m[n][b] ? fast_exp2(m[n][b] - x) : 1.f;  // m = -inf: 0
+          m[n][b] = x;
+          l[n][b] *= a[b];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[n][i][0] *= a[0], o[n][i][1] *= a[1];
+          o[n][i][2] *= a[0], o[n][i][3] *= a[1];
+        }
       }
     }
   }
   // Subtrahend of the exponent: w = 2^(x - base).
-  __device__ __forceinline__ float base(int r) const { return (m[r] == -CUDART_INF_F ? 0.f : m[r]) - kOffset; }
+  __device__ __forceinline__ float base(int n, int b) const {
+    return (m[n][b] == -CUDART_INF_F ? 0.f : m[n][b]) - kOffset;
+  }
 };
 
 // One block as the unit loop sees it.
@@ -227,113 +248,121 @@ struct Tile {
   int t0;         // first token of the request's part of the step
   int r0;         // first flattened row (token * G + group member) of the tile
   int nrows;      // flattened rows of the request
-  int max_pos;    // largest position among the tile's rows
 };
 
 template <int D>
 struct Layout {
   static constexpr int kStage = kPair * 2 * kUnit * D;  // bytes of a pair of units, K and V
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  static constexpr int kQ = 16 * (D + 8) * 2;           // bf16 queries, rows padded by 16 bytes
+  static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kList = kListCap * (int)sizeof(Entry);
-  static constexpr int bytes(int nw) { return kList + kQ + nw * kStages * kStage; }
+  static constexpr int q_bytes(int nt) { return 8 * nt * (D + 8) * 2; }  // bf16 queries, rows padded by 16 bytes
+  static constexpr int bytes(int nw, int nt) { return kList + q_bytes(nt) + nw * kStages * kStage; }
   static constexpr int kORow = D + 4;                   // floats per merged row: D, then m, l
   static_assert(16 * kORow * 4 <= kStages * kStage, "merge buffer fits the ring");
 };
 
-// One partial-block unit (16 tokens from `first` on, `n` of them real) from the tail.
-template <int D>
-__device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int first, int n, int pos_first,
-                                          const bf16* qs, const float* fac, const int* pos, State<D>& st, int g, int t) {
-  float s[2][4];
+// One unit of the partial block (16 tokens from `first` on; n tokens of the block are real) from the tail, as bf16.
+template <int D, int NT>
+__device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int first, int n_tok, int pos_first,
+                                          const bf16* qs, const int (*pos)[2], State<D, NT>& st, int g, int t) {
+  float s[NT][4];
+  const int r = first + (g >> 1) * 4 + (g & 1);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = first + (g >> 1) * 4 + 2 * i + (g & 1);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
+    for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
 #pragma unroll
-    for (int hh = 0; hh < D / 64; ++hh) {
-      uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (r < n) {
-        const uint4* src = reinterpret_cast<const uint4*>(tk + (size_t)r * D + 64 * hh + 16 * t);
-        w[0] = src[0], w[1] = src[1];
+  for (int hh = 0; hh < D / 64; ++hh) {
+    uint4 u[2][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      u[e][0] = u[e][1] = make_uint4(0, 0, 0, 0);
+      if (r + 2 * e < n_tok) {
+        const uint4* src = reinterpret_cast<const uint4*>(tk + (size_t)(r + 2 * e) * D + 64 * hh + 16 * t);
+        u[e][0] = src[0], u[e][1] = src[1];
       }
-      const uint32_t ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    }
+    const uint32_t us[8] = {u[0][0].x, u[0][0].y, u[0][0].z, u[0][0].w, u[0][1].x, u[0][1].y, u[0][1].z, u[0][1].w};
+    const uint32_t vs[8] = {u[1][0].x, u[1][0].y, u[1][0].z, u[1][0].w, u[1][1].x, u[1][1].y, u[1][1].z, u[1][1].w};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bf16* q0 = qs + g * (D + 8) + 64 * hh + 16 * t + 4 * x;
-        const bf16* q1 = q0 + 8 * (D + 8);
-        const uint2 a = *reinterpret_cast<const uint2*>(q0), b = *reinterpret_cast<const uint2*>(q1);
-        const uint32_t qa[4] = {a.x, b.x, a.y, b.y};
-        mma_bf16(s[i], qa, ws[2 * x], ws[2 * x + 1]);
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t a[4] = {us[2 * x], vs[2 * x], us[2 * x + 1], vs[2 * x + 1]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint2 b = *reinterpret_cast<const uint2*>(qs + (8 * n + g) * (D + 8) + 64 * hh + 16 * t + 4 * x);
+        mma_bf16(s[n], a, b.x, b.y);
       }
     }
   }
-  float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+  const float fac = kLog2e * rsqrtf((float)D);
+  float mx[NT][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int p = pos_first + first + 4 * t + 2 * i + (x & 1), r = x >> 1;
-      s[i][x] = p <= pos[r] && first + 4 * t + 2 * i + (x & 1) < n ? s[i][x] * fac[r] : -CUDART_INF_F;
-      mx[r] = fmaxf(mx[r], s[i][x]);
-    }
-  st.raise(mx[0], mx[1]);
-  const float base[2] = {st.base(0), st.base(1)};
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int n = 0; n < NT; ++n) {
+    mx[n][0] = mx[n][1] = -CUDART_INF_F;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      s[i][x] = fast_exp2(s[i][x] - base[x >> 1]);
-      st.l[x >> 1] += s[i][x] * (1.f / 32768.f);
+      const int tok = r + (x & 2), b = x & 1;
+      s[n][x] = tok < n_tok && pos_first + tok <= pos[n][b] ? s[n][x] * fac : -CUDART_INF_F;
+      mx[n][b] = fmaxf(mx[n][b], s[n][x]);
     }
-  uint32_t hi[4], lo[4];
+  }
+  st.raise(mx);
+  uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int n = 0; n < NT; ++n) {
+    const float base[2] = {st.base(n, 0), st.base(n, 1)};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float a = s[i][2 * r], b = s[i][2 * r + 1];
+    for (int x = 0; x < 4; ++x) {
+      s[n][x] = fast_exp2(s[n][x] - base[x & 1]);
+      st.l[n][x & 1] += s[n][x] * (1.f / 32768.f);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float a = s[n][2 * e], b = s[n][2 * e + 1];
       const uint32_t h = pack_bf16(a, b);
-      hi[2 * i + r] = h;
-      lo[2 * i + r] = pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+      hi[n][e] = transpose8x8(h);
+      lo[n][e] = transpose8x8(pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u)));
     }
+  }
 #pragma unroll
   for (int half = 0; half < D / 64; ++half) {  // 8 channels per lane at a time
     uint4 w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = first + 4 * t + i;
       w[i] = make_uint4(0, 0, 0, 0);
-      if (r < n) w[i] = *reinterpret_cast<const uint4*>(tv + (size_t)r * D + (D / 8) * g + 8 * half);
+      if (first + 4 * t + i < n_tok)
+        w[i] = *reinterpret_cast<const uint4*>(tv + (size_t)(first + 4 * t + i) * D + (D / 8) * g + 8 * half);
     }
     const uint32_t* ww[4] = {&w[0].x, &w[1].x, &w[2].x, &w[3].x};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a[4] = {__byte_perm(ww[0][i], ww[1][i], 0x5410), __byte_perm(ww[0][i], ww[1][i], 0x7632),
+                             __byte_perm(ww[2][i], ww[3][i], 0x5410), __byte_perm(ww[2][i], ww[3][i], 0x7632)};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t b0 = __byte_perm(ww[0][i], ww[1][i], e ? 0x7632 : 0x5410);
-        const uint32_t b1 = __byte_perm(ww[2][i], ww[3][i], e ? 0x7632 : 0x5410);
-        mma_bf16(st.o[8 * half + 2 * i + e], hi, b0, b1);
-        mma_bf16(st.o[8 * half + 2 * i + e], lo, b0, b1);
+      for (int n = 0; n < NT; ++n) {
+        mma_bf16(st.o[n][4 * half + i], a, hi[n][0], hi[n][1]);
+        mma_bf16(st.o[n][4 * half + i], a, lo[n][0], lo[n][1]);
       }
+    }
   }
 }
 
-// A CTA takes up to 16 query rows that read the same blocks: the query heads
+// A CTA takes up to 8 NT query rows that read the same blocks: the query heads
 // of a KV head's group over some tokens of one request (all blocks), or one
 // (token, query head) with its own list (selected).  Its warps take pairs of
 // units in turn, each with its own ring of copies in flight, and are merged at
 // the end; with several splits the split's result goes to `part`.
-template <int D, int KIND, int NW, bool SEL>
-__global__ void __launch_bounds__(NW * 32)
+template <int D, int KIND, int NW, int NT, bool SEL>
+__global__ void __launch_bounds__(NW * 32, NW == 4 ? (D == 128 ? 3 : 4) : 1)
 attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* __restrict__ sel, int topk,
             int per_token, int split_blocks, int nsplit, bf16* __restrict__ out, float* __restrict__ lse,
             float* __restrict__ part, int32_t* status) {
   using Ly = Layout<D>;
+  constexpr int TR = 8 * NT;  // rows of a tile
   extern __shared__ __align__(128) unsigned char smem[];
   Entry* list = reinterpret_cast<Entry*>(smem);
   bf16* qs = reinterpret_cast<bf16*>(smem + Ly::kList);
-  unsigned char* ring = smem + Ly::kList + Ly::kQ + (threadIdx.x >> 5) * Ly::kStages * Ly::kStage;
+  unsigned char* ring = smem + Ly::kList + Ly::q_bytes(NT) + (threadIdx.x >> 5) * Ly::kStages * Ly::kStage;
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int G = h_q / c.h_kv;
@@ -354,45 +383,55 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     split = blockIdx.z;
     const int u = blockIdx.x;
     if (per_token) {
-      const int tiles = (G + 15) / 16;
+      const int tiles = (G + TR - 1) / TR;
       T.t0 = u / tiles;
       T.row = __ldg(p.row + T.t0);
       if ((unsigned)T.row >= (unsigned)c.rows) return;
-      T.r0 = (u % tiles) * 16;
+      T.r0 = (u % tiles) * TR;
       T.nrows = G;
     } else {
       int lo = 0, hi = c.rows;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((long long)__ldg(p.cu + mid) * G / 16 + mid <= u) lo = mid; else hi = mid;
+        if ((long long)__ldg(p.cu + mid) * G / TR + mid <= u) lo = mid; else hi = mid;
       }
       T.row = lo;
       T.t0 = __ldg(p.cu + lo);
-      T.r0 = (int)(u - ((long long)T.t0 * G / 16 + lo)) * 16;
+      T.r0 = (int)(u - ((long long)T.t0 * G / TR + lo)) * TR;
       T.nrows = (min(__ldg(p.cu + lo + 1), p.T) - T.t0) * G;
       if (T.r0 >= T.nrows) return;
     }
   }
   const int len = c.state[2 * T.row], held = c.state[2 * T.row + 1];
-  const int rows = min(16, T.nrows - T.r0);  // real rows of the tile
+  const int rows = min(TR, T.nrows - T.r0);  // real rows of the tile
   // Position of a tile row; -1 for rows that see nothing.
   auto pos_of = [&](int r) {
     if (r >= rows) return -1;
     const int x = __ldg(p.pos + T.t0 + (T.r0 + r) / G);
     return x < len && x / c.B < held ? x : -1;
   };
-  int pos[2] = {pos_of(g), pos_of(g + 8)};
-  int mp = max(pos[0], pos[1]);
+  int pos[NT][2], mp = -1, min_pos = 0x7fffffff;
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) mp = max(mp, __shfl_xor_sync(~0u, mp, off));
-  T.max_pos = mp;
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int r = 8 * n + 2 * t + b;
+      pos[n][b] = pos_of(r);
+      mp = max(mp, pos[n][b]);
+      if (r < rows) min_pos = min(min_pos, pos[n][b]);
+    }
+#pragma unroll
+  for (int off = 1; off < 4; off <<= 1) {
+    mp = max(mp, __shfl_xor_sync(~0u, mp, off));
+    min_pos = min(min_pos, __shfl_xor_sync(~0u, min_pos, off));
+  }
   if (tid < rows && split == 0 && pos_of(tid) != __ldg(p.pos + T.t0 + (T.r0 + tid) / G)) set_status(status, kStatusBadTable);
 
   // ---- queries: bf16 in shared memory, fp16 fragments after scaling by a power of two
   auto item_of = [&](int r) {  // (token, query head) of a tile row
     return (size_t)(T.t0 + (T.r0 + r) / G) * h_q + T.head * G + (T.r0 + r) % G;
   };
-  for (int i = tid; i < 16 * (D / 8); i += NW * 32) {
+  for (int i = tid; i < TR * (D / 8); i += NW * 32) {
     const int r = i / (D / 8), ck = i % (D / 8);
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < rows) x = *reinterpret_cast<const uint4*>(q + item_of(r) * D + ck * 8);
@@ -410,43 +449,38 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     if (split > 0 && b0 >= b1) return;
   }
   __syncthreads();
-  uint32_t qf[D / 16][4];
-  float fac[2];
-  {
-    float am[2] = {0.f, 0.f};
-    uint2 raw[2][D / 16];
+  uint32_t qf[NT][D / 16][2];
+  float fac[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+  for (int n = 0; n < NT; ++n) {
+    float am = 0.f;
+    uint2 raw[D / 16];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        raw[r][k] = *reinterpret_cast<const uint2*>(qs + (g + 8 * r) * (D + 8) + 64 * (k / 4) + 16 * t + 4 * (k % 4));
-        const uint32_t w[2] = {raw[r][k].x, raw[r][k].y};
+    for (int k = 0; k < D / 16; ++k) {
+      raw[k] = *reinterpret_cast<const uint2*>(qs + (8 * n + g) * (D + 8) + 64 * (k / 4) + 16 * t + 4 * (k % 4));
+      const uint32_t w[2] = {raw[k].x, raw[k].y};
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          am[r] = fmaxf(am[r], fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-      }
+      for (int e = 0; e < 2; ++e)
+        am = fmaxf(am, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+    am = fmaxf(am, __shfl_xor_sync(~0u, am, 1));
+    am = fmaxf(am, __shfl_xor_sync(~0u, am, 2));
+    // exponent of the largest magnitude, kept where the factors are normal
+    const int e = max(-100, min(127, (int)((__float_as_uint(am) >> 23) & 255) - 127));
+    const float up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
+    const float down = __uint_as_float((uint32_t)(e - 8 + 127) << 23) * (kLog2e * rsqrtf((float)D));
+    fac[n][0] = __shfl_sync(~0u, down, 8 * t);      // of row 8 n + 2 t
+    fac[n][1] = __shfl_sync(~0u, down, 8 * t + 4);  // and the next
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      am[r] = fmaxf(am[r], __shfl_xor_sync(~0u, am[r], 1));
-      am[r] = fmaxf(am[r], __shfl_xor_sync(~0u, am[r], 2));
-      // exponent of the largest magnitude, kept where the factors are normal
-      const int e = max(-100, min(127, (int)((__float_as_uint(am[r]) >> 23) & 255) - 127));
-      const float up = __uint_as_float((uint32_t)(8 - e + 127) << 23);
-      fac[r] = __uint_as_float((uint32_t)(e - 8 + 127) << 23) * (kLog2e * rsqrtf((float)D));
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t w[2] = {raw[k].x, raw[k].y};
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t w[2] = {raw[r][k].x, raw[r][k].y};
-#pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2)
-          qf[k][2 * e2 + r] = pack_f16(__uint_as_float(w[e2] << 16) * up, __uint_as_float(w[e2] & 0xffff0000u) * up);
-      }
+      for (int e2 = 0; e2 < 2; ++e2)
+        qf[n][k][e2] = pack_f16(__uint_as_float(w[e2] << 16) * up, __uint_as_float(w[e2] & 0xffff0000u) * up);
     }
   }
-  int min_pos = min(g < rows ? pos[0] : 0x7fffffff, g + 8 < rows ? pos[1] : 0x7fffffff);
-#pragma unroll
-  for (int off = 4; off < 32; off <<= 1) min_pos = min(min_pos, __shfl_xor_sync(~0u, min_pos, off));
 
-  State<D> st;
+  State<D, NT> st;
   st.clear();
   const int upb = c.B / kUnit;
   const size_t page_bytes = (size_t)c.B * D;
@@ -530,9 +564,8 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     if (!tail_done) {
       const int n_tail = mp - own * c.B + 1;
       const size_t at = (((size_t)T.row * 2 + (own & 1)) * c.h_kv + T.head) * page_bytes;
-      const float f[2] = {kLog2e * rsqrtf((float)D), kLog2e * rsqrtf((float)D)};
       for (int u = (NW - 1 - warp); u * kUnit < n_tail; u += NW)
-        tail_unit<D>(c.tail_k + at, c.tail_v + at, u * kUnit, n_tail, own * c.B, qs, f, pos, st, g, t);
+        tail_unit<D, NT>(c.tail_k + at, c.tail_v + at, u * kUnit, n_tail, own * c.B, qs, pos, st, g, t);
       tail_done = true;
     }
     for (int i = 0; i < mine; ++i) {
@@ -540,47 +573,47 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       cp_async_wait<Ly::kStages - 1>();
       __syncwarp();
       const unsigned char* src = ring + (i % Ly::kStages) * Ly::kStage;
-      float s[2 * kPair][4];
-      float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+      float s[kPair][NT][4], mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -CUDART_INF_F;
 #pragma unroll
       for (int x = 0; x < kPair; ++x) {
         const int u = (warp + i * NW) * kPair + x;
-        unit_scores<D, KIND>(src + x * 2 * kUnit * D, qf, s + 2 * x, g, t);
+        unit_scores<D, KIND, NT>(src + x * 2 * kUnit * D, qf, s[x], g, t);
         const Entry e = list[u < units ? u / upb : 0];
         const int p0 = u < units && e.page >= 0 ? e.j * c.B + (u % upb) * kUnit : 0x7fffffff - kUnit;
-        const float f[2] = {fac[0] * e.ks, fac[1] * e.ks};
+        const int tok = p0 + 4 * (g >> 1) + (g & 1);
         const bool cut = p0 + kUnit - 1 > min_pos;
 #pragma unroll
-        for (int n8 = 0; n8 < 2; ++n8)
+        for (int n = 0; n < NT; ++n) {
+          const float f[2] = {fac[n][0] * e.ks, fac[n][1] * e.ks};
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            float& z = s[2 * x + n8][y];
-            z = fmaf(z, f[y >> 1], e.lv);
-            if (cut && p0 + 4 * t + 2 * n8 + (y & 1) > pos[y >> 1]) z = -CUDART_INF_F;
-            mx[y >> 1] = fmaxf(mx[y >> 1], z);
+            float& z = s[x][n][y];
+            z = fmaf(z, f[y & 1], e.lv);
+            if (cut && tok + (y & 2) > pos[n][y & 1]) z = -CUDART_INF_F;
+            mx[n][y & 1] = fmaxf(mx[n][y & 1], z);
           }
+        }
       }
-      st.raise(mx[0], mx[1]);
-      const float base[2] = {st.base(0), st.base(1)};
+      st.raise(mx);
 #pragma unroll
       for (int x = 0; x < kPair; ++x) {
         const int u = (warp + i * NW) * kPair + x;
         const float rest = list[u < units ? u / upb : 0].rest, inv = list[u < units ? u / upb : 0].inv;
-        uint32_t pf[4];
-        float sum[2] = {0.f, 0.f};
+        uint32_t pf[NT][2];
 #pragma unroll
-        for (int n8 = 0; n8 < 2; ++n8) {
-          float* z = s[2 * x + n8];
+        for (int n = 0; n < NT; ++n) {
+          float* z = s[x][n];
+          const float base[2] = {st.base(n, 0), st.base(n, 1)};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            z[y] = fast_exp2(z[y] - base[y >> 1]);
-            sum[y >> 1] += z[y];
-          }
-          pf[2 * n8] = pack_f16(z[0] * rest, z[1] * rest);
-          pf[2 * n8 + 1] = pack_f16(z[2] * rest, z[3] * rest);
+          for (int y = 0; y < 4; ++y) z[y] = fast_exp2(z[y] - base[y & 1]);
+          st.l[n][0] = fmaf(z[0] + z[2], inv, st.l[n][0]);
+          st.l[n][1] = fmaf(z[1] + z[3], inv, st.l[n][1]);
+          pf[n][0] = transpose8x8(pack_f16(z[0] * rest, z[1] * rest));
+          pf[n][1] = transpose8x8(pack_f16(z[2] * rest, z[3] * rest));
         }
-        st.l[0] += sum[0] * inv, st.l[1] += sum[1] * inv;
-        unit_values<D, KIND>(src + x * 2 * kUnit * D + kUnit * D, pf, st.o, g, t);
+        unit_values<D, KIND, NT>(src + x * 2 * kUnit * D + kUnit * D, pf, st.o, g, t);
       }
       __syncwarp();
     }
@@ -590,26 +623,25 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   } while (!SEL && done < n_list);
 
   // ---- merge the warps
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    st.l[r] += __shfl_xor_sync(~0u, st.l[r], 1);
-    st.l[r] += __shfl_xor_sync(~0u, st.l[r], 2);
-  }
   float* buf = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    float* b = buf + (g + 8 * r) * Ly::kORow;
-    if (g + 8 * r < rows) {
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        b[(D / 8) * (2 * t) + i] = st.o[i][2 * r];
-        b[(D / 8) * (2 * t + 1) + i] = st.o[i][2 * r + 1];
+    for (int b = 0; b < 2; ++b) {
+      float l = st.l[n][b];
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(~0u, l, off);
+      const int r = 8 * n + 2 * t + b;
+      if (r < rows) {
+        float* d = buf + r * Ly::kORow;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(d + (D / 8) * g + 2 * i) = make_float2(st.o[n][i][b], st.o[n][i][2 + b]);
+        if (g == 0) d[D] = st.m[n][b], d[D + 1] = l;
       }
-      if (t == 0) b[D] = st.m[r], b[D + 1] = st.l[r];
     }
-  }
   __syncthreads();
-  const float* all = reinterpret_cast<const float*>(smem + Ly::kList + Ly::kQ);
+  const float* all = reinterpret_cast<const float*>(smem + Ly::kList + Ly::q_bytes(NT));
   constexpr int kStep = Ly::kStages * Ly::kStage / 4;
   for (int i = tid; i < rows * (D / 4); i += NW * 32) {
     const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
@@ -675,29 +707,31 @@ merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float*
 
 // How a step over all blocks is cut up.
 struct Cut {
-  bool many;       // tiles of 128 rows (cache_attn_rows.cu) instead of 16
-  bool per_token;  // tiles of 16: each token on its own, or a request's tokens together, whichever bound is less
+  bool many;       // tiles of 128 rows (cache_attn_rows.cu)
+  bool wide;       // tiles of 16 rows instead of 8
+  bool per_token;  // each token on its own, or a request's tokens together, whichever bound is less
   long long tiles;
   int split_blocks, nsplit;
 };
 
-// Long rows are cut into splits of whole blocks, so that even few tiles fill
-// the GPU: about four CTAs per SM counted over rows of full length, and at
-// least 512 tokens each (a split costs a partial result of D + 4 floats per
-// query row, written and read back).
+// Long rows are cut into splits of whole blocks, so that even few or uneven
+// rows fill the GPU: about 16 CTAs per SM counted over rows of full length
+// (tiles of 128 rows: 4), and at least 1024 tokens each (512): a split costs a
+// partial result of D + 4 floats per query row, written and read back.
 Cut cut_of(const View& c, int T, int h_q) {
   const int G = h_q / c.h_kv;
   const long long a = (long long)T * ((G + 15) / 16), b = (long long)T * G / 16 + c.rows;
   const long long big = (long long)T * G / 128 + (T < c.rows ? T : c.rows);
   Cut x;
   x.per_token = a <= b;
+  x.wide = !x.per_token || G > 8;
   x.tiles = x.per_token ? a : b;
   x.many = x.tiles >= 2 * big;
   if (x.many) x.tiles = (long long)T * G / 128 + c.rows;
   const long long ctas = (x.many ? big : x.tiles) * c.h_kv;
-  const long long want = ((x.many ? 6 : 4) * 148 + ctas - 1) / ctas;
+  const long long want = ((x.many ? 4 : 16) * 148 + ctas - 1) / ctas;
   const long long step = x.many && c.B < 128 ? 128 / c.B : 1;  // splits of whole key tiles
-  const long long least = (512 + c.B - 1) / c.B;
+  const long long least = (x.many ? 512 : 1024) / c.B;
   long long blocks = (c.max_blocks + want - 1) / want;
   if (blocks < least) blocks = least;
   blocks = (blocks + step - 1) / step * step;
@@ -706,44 +740,41 @@ Cut cut_of(const View& c, int T, int h_q) {
   return x;
 }
 
+template <int D, int KIND, int NW, int NT, bool SEL>
+cudaError_t launch_one(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk, dim3 grid,
+                       int per_token, int split_blocks, int nsplit, bf16* out, float* lse, float* part, int32_t* status,
+                       cudaStream_t st) {
+  constexpr int smem = Layout<D>::bytes(NW, NT);
+  const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, NT, SEL>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_kernel<D, KIND, NW, NT, SEL><<<grid, NW * 32, smem, st>>>(c, p, q, h_q, sel, topk, per_token, split_blocks, nsplit,
+                                                                 out, lse, part, status);
+  return cudaGetLastError();
+}
+
 template <int D, int KIND>
 cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk, bf16* out,
                        float* lse, float* part, int32_t* status, cudaStream_t st) {
-  using Ly = Layout<D>;
-  cudaError_t e;
   if (sel) {
     const dim3 grid(p.T, h_q);
     // few rows: more warps each, so that their blocks are read at once
-    if ((long long)p.T * h_q > 2 * 148) {
-      constexpr int NW = 4;
-      if ((e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Ly::bytes(NW))) != cudaSuccess)
-        return e;
-      attn_kernel<D, KIND, NW, true><<<grid, NW * 32, Ly::bytes(NW), st>>>(c, p, q, h_q, sel, topk, 0, 0, 1, out, lse,
-                                                                          nullptr, status);
-    } else {
-      constexpr int NW = 8;
-      if ((e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    Ly::bytes(NW))) != cudaSuccess)
-        return e;
-      attn_kernel<D, KIND, NW, true><<<grid, NW * 32, Ly::bytes(NW), st>>>(c, p, q, h_q, sel, topk, 0, 0, 1, out, lse,
-                                                                          nullptr, status);
-    }
-    return cudaGetLastError();
+    if ((long long)p.T * h_q > 2 * 148)
+      return launch_one<D, KIND, 4, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
+    return launch_one<D, KIND, 8, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
   }
   const Cut x = cut_of(c, p.T, h_q);
-  if (x.many) {
+  const dim3 grid((unsigned)x.tiles, c.h_kv, x.nsplit);
+  cudaError_t e;
+  if (x.many)
     e = launch_attention_rows(c, p, q, h_q, (int)x.tiles, x.split_blocks, x.nsplit, out, lse, part, status, st);
-    if (e != cudaSuccess || x.nsplit == 1) return e;
-  } else {
-    constexpr int NW = 4;
-    if ((e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  Ly::bytes(NW))) != cudaSuccess)
-      return e;
-    attn_kernel<D, KIND, NW, false><<<dim3((unsigned)x.tiles, c.h_kv, x.nsplit), NW * 32, Ly::bytes(NW), st>>>(
-        c, p, q, h_q, nullptr, 0, x.per_token, x.split_blocks, x.nsplit, out, lse, part, status);
-    if ((e = cudaGetLastError()) != cudaSuccess || x.nsplit == 1) return e;
-  }
+  else if (x.wide)
+    e = launch_one<D, KIND, 4, 2, false>(c, p, q, h_q, nullptr, 0, grid, x.per_token, x.split_blocks, x.nsplit, out, lse,
+                                         part, status, st);
+  else
+    e = launch_one<D, KIND, 4, 1, false>(c, p, q, h_q, nullptr, 0, grid, x.per_token, x.split_blocks, x.nsplit, out, lse,
+                                         part, status, st);
+  if (e != cudaSuccess || x.nsplit == 1) return e;
   const long long items = (long long)p.T * h_q;
   merge_kernel<D><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
   return cudaGetLastError();
