@@ -227,19 +227,19 @@ struct State {
 
 // One block as the unit loop sees it.
 struct __align__(16) Entry {
-  int page;  // -1: skip
-  int j;
+  long long at;  // byte offset of its K and V tiles; -1: skip
+  int pos;       // position of its first token
   float ks;
-  float lv;    // log2 of the V scale, taken as at least 2^-100
-  float rest;  // V scale over that (1 but for smaller scales)
-  float inv;   // 2^-15 over that
-  float pad[2];
+  float lv;      // log2 of the V scale, taken as at least 2^-100
+  float rest;    // V scale over that (1 but for smaller scales)
+  float inv;     // 2^-15 over that
+  float pad;
 };
 
 __device__ __forceinline__ Entry make_entry(const View& c, int page, int j, int head) {
   const size_t at = (size_t)page * c.h_kv + head;
   const float s = __ldg(c.v_scale + at), vs = fmaxf(s, 7.8886090522101181e-31f);
-  return Entry{page, j, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 32768.f) / vs, {0.f, 0.f}};
+  return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 32768.f) / vs, 0.f};
 }
 
 struct Tile {
@@ -366,6 +366,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int G = h_q / c.h_kv;
+  const int lb = 31 - __clz(c.B), lu = lb - 4;  // log2 of the tokens and units of a block
 
   // ---- the tile
   Tile T;
@@ -408,7 +409,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   auto pos_of = [&](int r) {
     if (r >= rows) return -1;
     const int x = __ldg(p.pos + T.t0 + (T.r0 + r) / G);
-    return x < len && x / c.B < held ? x : -1;
+    return x < len && x >> lb < held ? x : -1;
   };
   int pos[NT][2], mp = -1, min_pos = 0x7fffffff;
 #pragma unroll
@@ -437,7 +438,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     if (r < rows) x = *reinterpret_cast<const uint4*>(q + item_of(r) * D + ck * 8);
     *reinterpret_cast<uint4*>(qs + r * (D + 8) + ck * 8) = x;
   }
-  const int own = mp < 0 ? -1 : mp / c.B;
+  const int own = mp < 0 ? -1 : mp >> lb;
   const bool tail = own >= 0 && (long long)(own + 1) * c.B > len;  // the last block is partial
   int b0 = 0, b1 = own + 1;                                        // blocks of this CTA
   bool my_tail = tail;
@@ -482,7 +483,6 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
 
   State<D, NT> st;
   st.clear();
-  const int upb = c.B / kUnit;
   const size_t page_bytes = (size_t)c.B * D;
   bool tail_done = !my_tail;
 
@@ -530,7 +530,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
         const int j = b0 + done + e;
         const int pg = block_page(c, T.row, j);
         if (pg < 0) set_status(status, kStatusBadTable);
-        list[e] = pg >= 0 ? make_entry(c, pg, j, T.head) : Entry{-1, j, 0.f, 0.f, 0.f, 0.f, {0.f, 0.f}};
+        list[e] = pg >= 0 ? make_entry(c, pg, j, T.head) : Entry{-1, j * c.B, 0.f, 0.f, 0.f, 0.f, 0.f};
       }
     }
     __syncthreads();
@@ -540,8 +540,8 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       tail_done = !(s_count >> 16);
     }
     // Units of the listed blocks; the last one may end before its block does.
-    int units = count * upb;
-    if (count > 0 && list[count - 1].j == own) units -= upb - (mp - own * c.B) / kUnit - 1;
+    int units = count << lu;
+    if (count > 0 && list[count - 1].pos == own * c.B) units -= (1 << lu) - (mp - own * c.B) / kUnit - 1;
     const int pairs = (units + kPair - 1) / kPair;
     const int mine = warp < pairs ? (pairs - warp + NW - 1) / NW : 0;
     auto fetch = [&](int i) {
@@ -550,9 +550,9 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
 #pragma unroll
         for (int x = 0; x < kPair; ++x) {
           const int u = (warp + i * NW) * kPair + x;
-          const Entry e = list[u < units ? u / upb : 0];
-          const bool ok = u < units && e.page >= 0;
-          const size_t at = ok ? ((size_t)e.page * c.h_kv + T.head) * page_bytes + (size_t)(u % upb) * (kUnit * D) : 0;
+          const long long off = list[u < units ? u >> lu : 0].at;
+          const bool ok = u < units && off >= 0;
+          const size_t at = ok ? off + (u & ((1 << lu) - 1)) * (kUnit * D) : 0;
           fetch_unit<D>(dst + x * 2 * kUnit * D, c.k + at, c.v + at, ok, lane);
         }
       }
@@ -580,8 +580,8 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       for (int x = 0; x < kPair; ++x) {
         const int u = (warp + i * NW) * kPair + x;
         unit_scores<D, KIND, NT>(src + x * 2 * kUnit * D, qf, s[x], g, t);
-        const Entry e = list[u < units ? u / upb : 0];
-        const int p0 = u < units && e.page >= 0 ? e.j * c.B + (u % upb) * kUnit : 0x7fffffff - kUnit;
+        const Entry e = list[u < units ? u >> lu : 0];
+        const int p0 = u < units && e.at >= 0 ? e.pos + (u & ((1 << lu) - 1)) * kUnit : 0x7fffffff - kUnit;
         const int tok = p0 + 4 * (g >> 1) + (g & 1);
         const bool cut = p0 + kUnit - 1 > min_pos;
 #pragma unroll
@@ -591,16 +591,26 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
           for (int y = 0; y < 4; ++y) {
             float& z = s[x][n][y];
             z = fmaf(z, f[y & 1], e.lv);
-            if (cut && tok + (y & 2) > pos[n][y & 1]) z = -CUDART_INF_F;
-            mx[n][y & 1] = fmaxf(mx[n][y & 1], z);
           }
+        }
+        if (cut) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (tok + (y & 2) > pos[n][y & 1]) s[x][n][y] = -CUDART_INF_F;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mx[n][0] = fmaxf(mx[n][0], fmaxf(s[x][n][0], s[x][n][2]));
+          mx[n][1] = fmaxf(mx[n][1], fmaxf(s[x][n][1], s[x][n][3]));
         }
       }
       st.raise(mx);
 #pragma unroll
       for (int x = 0; x < kPair; ++x) {
         const int u = (warp + i * NW) * kPair + x;
-        const float rest = list[u < units ? u / upb : 0].rest, inv = list[u < units ? u / upb : 0].inv;
+        const float rest = list[u < units ? u >> lu : 0].rest, inv = list[u < units ? u >> lu : 0].inv;
         uint32_t pf[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {

@@ -156,6 +156,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const uint32_t mb_k = sbase + Ly::MB_OFF, mb_v = mb_k + 8, mb_s = mb_k + 16, mb_p = mb_k + 24, mb_o = mb_k + 32;
   volatile int* fail = reinterpret_cast<volatile int*>(sm + Ly::FAIL_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lb = 31 - __clz(c.B);
   const int G = h_q / c.h_kv, head = blockIdx.y, split = blockIdx.z, u0 = blockIdx.x;
 
   // ---- the tile's rows
@@ -172,11 +173,11 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const int len = c.state[2 * row], held = c.state[2 * row + 1];
   auto pos_of = [&](int r) {
     const int x = __ldg(p.pos + t0 + (r0 + r) / G);
-    return x < len && x / c.B < held ? x : -1;
+    return x < len && x >> lb < held ? x : -1;
   };
   // positions ascend along a request's tokens
   const int mp = pos_of(rows - 1);
-  const int own = mp < 0 ? -1 : mp / c.B;
+  const int own = mp < 0 ? -1 : mp >> lb;
   const int b0 = min(own + 1, split * split_blocks), b1 = min(own + 1, b0 + split_blocks);
   if (split > 0 && b0 >= b1) return;
   const int kt0 = b0 * c.B / kKeys;                                  // split_blocks * B is a multiple of kKeys
@@ -261,7 +262,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     // A unit's table entry (only loaded here: nothing waits for it), and what it says: page; -1: zeros; -2: tail.
     auto unit_entry = [&](int i, int x) {
       const int ps = unit_pos(i, x);
-      return i < nt && ps < kend && ps < tail0 ? __ldg(c.table + (size_t)row * c.max_blocks + ps / c.B) : 0;
+      return i < nt && ps < kend && ps < tail0 ? __ldg(c.table + (size_t)row * c.max_blocks + (ps >> lb)) : 0;
     };
     auto unit_page = [&](int entry, int i, int x) {
       const int ps = unit_pos(i, x);
@@ -273,7 +274,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     };
     // address of a unit's codes inside the pages
     auto unit_at = [&](int pg, int i, int x) {
-      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) % c.B) * D + code_at;
+      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) & (c.B - 1)) * D + code_at;
     };
     auto put = [&](uint32_t base, int x, int z, uint4 a, uint4 b) {
       unsigned char* dst = sm + base + (z % Ly::KB) * Ly::REGION + (2 * (2 * pw + x) + z / Ly::KB) * 1024;
