@@ -9,13 +9,16 @@
 // largest such bound over a row's blocks, any value b that at least K = topk - 1
 // screen scores reach gives: every block of the true top K has a screen score
 // >= b - 2 e.  Kernel one writes the screen scores (mma.m16n8k16, bf16, tiles
-// of 16 query rows of one request and KV head against 8 blocks); kernel two
-// takes as b the K-th largest of the 128 maxima its threads find in disjoint
-// subsets (about 1.1 K blocks pass), scores the passing blocks in 64 bits, and
-// ranks them by (score, block).  Products of bf16 are exact in 64 bits and
-// their sums are off by 2^-46 at most, so the result is that of exact
+// of 16 query rows of one request and KV head against 8 blocks); in kernel two
+// a warp takes a query row: b is the K-th largest of the maxima of 128 disjoint
+// subsets (about 1.1 K blocks pass), passing blocks whose screen score is more
+// than 2 e above the K-th largest are in, and the few others are scored in 64
+// bits and ranked by (score, block).  Products of bf16 are exact in 64 bits
+// and their sums are off by 2^-46 at most, so the result is that of exact
 // arithmetic unless two scores agree to 14 digits.
 #include <math_constants.h>
+
+#include <climits>
 
 #include "cache.cuh"
 
@@ -24,8 +27,10 @@ namespace cache {
 namespace {
 
 constexpr int kScoreThreads = 128;
-constexpr int kSelThreads = 128;
-constexpr int kCand = 512;       // candidates ranked at a time
+constexpr int kSelWarps = 4;
+constexpr int kCand = 256;       // candidates held per warp (at most 32 x 32)
+constexpr int kHeld = 16;        // pieces of 4 screen scores per lane and batch
+constexpr float kNone = -3.4e38f; // below every finite screen score that can win
 constexpr size_t kScratch = (size_t)256 << 20;  // screen scores held at a time
 
 struct Slab {
@@ -44,11 +49,11 @@ __device__ __forceinline__ int tile_base(const Plan& p, const Slab& s, int r, in
   return (int)((long long)(clip(__ldg(p.cu + r), s) - s.t0) * G / 16) + r;
 }
 
-// Number of earlier blocks of a token, or -1 (sees nothing), -2 (plan entry out of range).
-__device__ __forceinline__ int own_block(const View& c, const Plan& p, int row, int tok) {
-  const int pos = __ldg(p.pos + tok);
+// Number of earlier blocks of a token at `pos`, or -1 (sees nothing), -2 (plan entry out of range).
+__device__ __forceinline__ int own_block(const View& c, int row, int pos) {
   if (pos < 0) return -1;
-  return pos < c.state[2 * row] && pos / c.B < c.state[2 * row + 1] ? pos / c.B : -2;
+  const int j = pos >> (31 - __clz(c.B));
+  return pos < c.state[2 * row] && j < c.state[2 * row + 1] ? j : -2;
 }
 
 template <int D>
@@ -82,7 +87,7 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
   }
   const int rows = min(16, nrows - r0);
   int nb = 0;
-  if (lane < rows) nb = max(0, own_block(c, p, row, tok0 + (r0 + lane) / G));
+  if (lane < rows) nb = max(0, own_block(c, row, __ldg(p.pos + tok0 + (r0 + lane) / G)));
   for (int off = 1; off < 16; off <<= 1) nb = max(nb, __shfl_xor_sync(~0u, nb, off));
   nb = __shfl_sync(~0u, nb, 0);
   const int j0 = blockIdx.z * sl.chunk, j1 = min(nb, j0 + sl.chunk);
@@ -105,6 +110,10 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
     qf[k][0] = x.x, qf[k][1] = y.x, qf[k][2] = x.y, qf[k][3] = y.y;
   }
   float most = 0.f;
+  float* dst[2];  // screen scores of this lane's rows
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    dst[r] = g + 8 * r < rows ? score + (item_of(g + 8 * r) - (size_t)sl.t0 * h_q) * sl.stride + 2 * t : nullptr;
   for (int j = j0 + warp * NT * 8; j < j1; j += kScoreThreads / 32 * NT * 8) {
     int mine = -1;
     if (j + lane < j1) {
@@ -142,10 +151,9 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
       const int jj = j + n * 8 + 2 * t;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        if (g + 8 * r < rows) {
-          float* dst = score + item_of(g + 8 * r) * sl.stride - (size_t)sl.t0 * h_q * sl.stride + jj;
-          if (jj + 1 < j1) *reinterpret_cast<float2*>(dst) = make_float2(s[2 * r], s[2 * r + 1]);
-          else if (jj < j1) *dst = s[2 * r];
+        if (dst[r]) {
+          if (jj + 1 < j1) *reinterpret_cast<float2*>(dst[r] + j + n * 8) = make_float2(s[2 * r], s[2 * r + 1]);
+          else if (jj < j1) dst[r][j + n * 8] = s[2 * r];
         }
     }
   }
@@ -161,181 +169,352 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
   }
 }
 
-// 64-bit scores of candidates [from, n): 8 lanes each.
-template <int D>
-__device__ void rescore(const View& c, int row, int head, const bf16* q, const int* cj, double* cs, int from, int n) {
-  const int sub = threadIdx.x & 7;
-  for (int base = from; base < n; base += kSelThreads / 8) {
-    const int i = base + (threadIdx.x >> 3);
-    double s = 0.0;
-    if (i < n) {
-      const int pg = block_page(c, row, cj[i]);
-      if (pg >= 0) {
-        const bf16* hi = c.cent + ((size_t)pg * c.h_kv + head) * D + sub * (D / 8);
-        const bf16* lo = hi + (size_t)c.n_pages * c.h_kv * D;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          float a[8], b[8], y[8];
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(hi) + x), a);
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(lo) + x), b);
-          bf16x8_to_f32(*reinterpret_cast<const uint4*>(q + sub * (D / 8) + 8 * x), y);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) s += (double)y[k] * ((double)a[k] + (double)b[k]);
-        }
-      } else {
-        s = -CUDART_INF;
-      }
-    }
-    for (int off = 1; off < 8; off <<= 1) s += __shfl_xor_sync(~0u, s, off);
-    if (i < n && sub == 0) cs[i] = isnan(s) ? -CUDART_INF : s;
-  }
+// Order-preserving key of a float that is not NaN, and back.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
+
+// Order-preserving whole number of a score (comparing doubles takes several times as long); NaN counts as -infinity,
+// -0 as 0.
+__device__ __forceinline__ long long order_of(double s) {
+  const long long b = __double_as_longlong(s + 0.0);
+  return isnan(s) ? LLONG_MIN : b ^ ((b >> 63) & LLONG_MAX);
 }
 
+// One warp's candidates.
+struct List {
+  long long exact[kCand];  // order_of an exact score
+  float screen[kCand];
+  int j[kCand];
+  int todo[kCand];         // list positions of the candidates being scored,
+  int page[kCand];         // their pages, then the upper words of their exact scores
+  int count;
+};
+
+// 64-bit scores of the candidates i < n for which `want(i)`, 16 at a time (2 lanes each); their list positions stay in
+// todo, the upper words of their scores in page; returns their number.
+template <int D, typename F>
+__device__ __forceinline__ int rescore(const View& c, int row, int head, const bf16* q, List& ls, int n, F want) {
+  constexpr int V = D / 16;  // 16-byte pieces per lane
+  const int lane = threadIdx.x & 31, sub = lane & 1;
+  int m = 0;
+  for (int x = 0; x < n; x += 32) {
+    const bool w = x + lane < n && want(x + lane);
+    const int pg = w ? block_page(c, row, ls.j[x + lane]) : -1;
+    const uint32_t b = __ballot_sync(~0u, w);
+    const int at = m + __popc(b & ((1u << lane) - 1));
+    if (w) ls.todo[at] = x + lane, ls.page[at] = pg;
+    m += __popc(b);
+  }
+  __syncwarp();
+  for (int base = 0; base < m; base += 16) {
+    const int k = base + (lane >> 1);
+    const int pg = k < m ? ls.page[k] : -1;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    if (pg >= 0) {
+      const uint4* hi = reinterpret_cast<const uint4*>(c.cent + ((size_t)pg * c.h_kv + head) * D) + sub;
+      const uint4* lo = hi + (size_t)c.n_pages * c.h_kv * (D / 8);
+      uint4 u[V], v[V];
+#pragma unroll
+      for (int x = 0; x < V; ++x) u[x] = __ldg(hi + 2 * x), v[x] = __ldg(lo + 2 * x);
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        float a[8], b[8], f[8];
+        bf16x8_to_f32(u[x], a);
+        bf16x8_to_f32(v[x], b);
+        bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(q) + sub + 2 * x), f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e & 3] += (double)f[e] * ((double)a[e] + (double)b[e]);
+      }
+    }
+    double r = (s[0] + s[1]) + (s[2] + s[3]);
+    r += __shfl_xor_sync(~0u, r, 1);
+    if (k < m && sub == 0) {
+      const long long o = pg < 0 ? LLONG_MIN : order_of(r);
+      ls.exact[ls.todo[k]] = o;
+      ls.page[k] = (int)(o >> 32);
+    }
+  }
+  __syncwarp();
+  return m;
+}
+
+// Whether candidate (s, j) is among the best K of the list positions todo[0, m) (all positions when todo is null).
+__device__ __forceinline__ bool among(const List& ls, const int* todo, int m, int K, long long s, int j) {
+  int above = 0;
+#pragma unroll 4
+  for (int k = 0; k < m; ++k) {
+    const int i = todo ? todo[k] : k;
+    const long long o = ls.exact[i];
+    above += o > s || (o == s && ls.j[i] < j);
+  }
+  return above < K;
+}
+
+// Rows with more candidates than the list holds, or screen scores that do not count (bar = -infinity): blocks in
+// order, all that reach the bar scored in 64 bits, the best K staying whenever the list is full.  Returns how many are
+// in the list; all have their exact scores.
 template <int D>
-__global__ void __launch_bounds__(kSelThreads)
+__device__ __noinline__ int many_candidates(const View& c, int row, int head, const bf16* q, List& ls, const float* sc,
+                                            int own, float bar, int K) {
+  const int lane = threadIdx.x & 31;
+  int n = 0, scored = 0;
+  for (int base = 0; base < own; base += 32) {
+    const int j = base + lane;
+    const bool in = j < own && (bar == -CUDART_INF_F || sc[j] >= bar);
+    const uint32_t m = __ballot_sync(~0u, in);
+    if (in) ls.j[n + __popc(m & ((1u << lane) - 1))] = j;
+    n += __popc(m);
+    __syncwarp();
+    if (n > kCand - 32) {
+      rescore<D>(c, row, head, q, ls, n, [&](int i) { return i >= scored; });
+      uint32_t keep = 0;  // ranks need the whole list: first all of them, then the moves
+      for (int x = 0; x * 32 < n; ++x) {
+        const int i = x * 32 + lane;
+        if (i < n && among(ls, nullptr, n, K, ls.exact[i], ls.j[i])) keep |= 1u << x;
+      }
+      __syncwarp();
+      int kept = 0;
+      for (int x = 0; x * 32 < n; ++x) {
+        const bool k = keep >> x & 1;
+        const long long s = k ? ls.exact[x * 32 + lane] : 0;
+        const int jj = k ? ls.j[x * 32 + lane] : 0;
+        const uint32_t b = __ballot_sync(~0u, k);
+        const int at = kept + __popc(b & ((1u << lane) - 1));  // at most x * 32 + lane
+        __syncwarp();
+        if (k) ls.exact[at] = s, ls.j[at] = jj;
+        kept += __popc(b);
+      }
+      __syncwarp();
+      n = scored = kept;
+    }
+  }
+  rescore<D>(c, row, head, q, ls, n, [&](int i) { return i >= scored; });
+  return n;
+}
+
+// The K-th largest of the warp's keys (N per lane; at least K of them real), to 16 bits (a bf16) from below: two bits a
+// step, the three counts in one sum.
+template <int N>
+__device__ __forceinline__ uint32_t kth_key(const uint32_t* key, int K) {
+  uint32_t b = 0;
+#pragma unroll 1
+  for (int bit = 30; bit >= 16; bit -= 2) {
+    uint32_t cnt = 0;
+#pragma unroll
+    for (int x = 0; x < N; ++x)
+#pragma unroll
+      for (int s = 1; s < 4; ++s) cnt += (uint32_t)(key[x] >= (b | (uint32_t)s << bit)) << (10 * (s - 1));
+    cnt = __reduce_add_sync(~0u, cnt);  // at most 32 N = 256 each
+    const int s = ((int)(cnt & 1023) >= K) + ((int)(cnt >> 10 & 1023) >= K) + ((int)(cnt >> 20) >= K);
+    b |= (uint32_t)s << bit;
+  }
+  return b;
+}
+
+// One warp per (token, query head).
+template <int D>
+__global__ void __launch_bounds__(kSelWarps * 32)
 select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int topk, const float* __restrict__ score,
               const float* __restrict__ hmax, int32_t* __restrict__ sel, int32_t* status) {
-  __shared__ __align__(16) bf16 qs[D];
-  __shared__ float top[kSelThreads];
-  __shared__ double cs[kCand];
-  __shared__ int cj[kCand];
-  __shared__ int n_cand;
-  __shared__ float s_b, s_norm;
-  const int tid = threadIdx.x, lane = tid & 31, h = blockIdx.y;
-  const int tok = sl.t0 + blockIdx.x;
-  const int row = __ldg(p.row + tok);
-  if ((unsigned)row >= (unsigned)c.rows) return;
+  __shared__ List lists[kSelWarps];
+  const int lane = threadIdx.x & 31;
+  List& ls = lists[threadIdx.x >> 5];
+  const int local = blockIdx.x * kSelWarps + (threadIdx.x >> 5);  // item of the slab
+  if (local >= (sl.t1 - sl.t0) * h_q) return;
+  const int tok = sl.t0 + local / h_q, h = local % h_q;
   const size_t item = (size_t)tok * h_q + h;
+  const bf16* qr = q + item * D;
+  uint32_t qw[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) qw[i] = __ldg(reinterpret_cast<const uint32_t*>(qr) + lane + 32 * i);
+  const int row = __ldg(p.row + tok), pos = __ldg(p.pos + tok);
+  if ((unsigned)row >= (unsigned)c.rows) return;
   int32_t* out = sel + item * topk;
-  const int own = own_block(c, p, row, tok);
-  if (own < 0) {
-    if (own == -2 && tid == 0) set_status(status, kStatusBadTable);
-    if (tid < topk) out[tid] = -1;
-    return;
-  }
+  const int own = own_block(c, row, pos);
   const int K = topk - 1;
-  if (own <= K) {  // every earlier block
-    if (tid < topk) out[tid] = tid <= own ? tid : -1;
+  if (own <= K) {  // every earlier block; none (-1) for a token that sees nothing
+    if (own == -2 && lane == 0) set_status(status, kStatusBadTable);
+    for (int i = lane; i < topk; i += 32) out[i] = i <= own ? i : -1;
     return;
   }
   if (K == 0) {
-    if (tid == 0) out[0] = own;
+    if (lane == 0) out[0] = own;
     return;
   }
   const int G = h_q / c.h_kv, head = h / G;
-  const float* sc = score + ((size_t)blockIdx.x * h_q + h) * sl.stride;
-  // ---- error bound e, and b
-  if (tid < 32) {
-    float sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const bf16 x = q[item * D + lane * (D / 32) + i];
-      qs[lane * (D / 32) + i] = x;
-      const float f = __bfloat162float(x);
-      sq = fmaf(f, f, sq);
-    }
-    for (int off = 16; off; off >>= 1) sq += __shfl_xor_sync(~0u, sq, off);
-    int tile;
-    if (sl.per_token) {
-      tile = (tok - sl.t0) * ((G + 15) / 16) + (h % G) / 16;
-    } else {
-      tile = tile_base(p, sl, row, G) + ((tok - clip(__ldg(p.cu + row), sl)) * G + h % G) / 16;
-    }
-    float m = 0.f;
-    bool bad = false;
-    for (int i = lane; i * sl.chunk < own; i += 32) {
-      const float x = hmax[((size_t)tile * c.h_kv + head) * sl.nchunk + i];
-      bad |= !(x <= 3.0e38f);
-      m = fmaxf(m, x);
-    }
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, off));
-    bad = __any_sync(~0u, bad) || !(sq <= 3.0e38f);
-    // |q| max |hi| (2^-8 + 2^-10), and room for products below the normal range
-    if (lane == 0) s_norm = bad ? CUDART_INF_F : sqrtf(sq) * sqrtf(m) * 4.8828125e-3f + 1e-30f;
-  }
-  float mx = -CUDART_INF_F;
-  bool odd = false;  // a screen score that is not finite
-  for (int j = tid; j < own; j += kSelThreads) {
-    const float s = sc[j];
-    odd |= !(fabsf(s) <= 3.0e38f);
-    mx = fmaxf(mx, s);
-  }
-  top[tid] = mx;
-  if (tid == 0) s_b = -CUDART_INF_F, n_cand = 0;
-  odd = __syncthreads_or(odd);
-  if (tid < own) {  // K < own subsets hold a block; the K-th largest maximum has K - 1 above or beside it
-    int above = 0, same = 0;
-#pragma unroll 8
-    for (int i = 0; i < kSelThreads; ++i) {
-      above += top[i] > mx;
-      same += top[i] == mx;
-    }
-    if (above < K && above + same >= K) s_b = mx;
-  }
-  __syncthreads();
-  const float e2 = 2.f * s_norm;
-  const float bar = odd || !(e2 <= 3.0e38f) ? -CUDART_INF_F : s_b - e2;
-  // ---- candidates; when the list is full the best K of it stay
-  auto keep_best = [&](int from) {  // cj[0, n) with exact scores below `from`
-    __syncthreads();
-    const int n = n_cand;
-    rescore<D>(c, row, head, qs, cj, cs, from, n);
-    __syncthreads();
-    double ks[kCand / kSelThreads];
-    int kj[kCand / kSelThreads], kr[kCand / kSelThreads];
-#pragma unroll
-    for (int x = 0; x < kCand / kSelThreads; ++x) {
-      const int i = tid + x * kSelThreads;
-      kr[x] = K;
-      if (i < n) {
-        const double s = cs[i];
-        const int j = cj[i];
-        int above = 0;
-        for (int k = 0; k < n; ++k) {
-          const double o = cs[k];
-          above += o > s || (o == s && cj[k] < j);
-        }
-        ks[x] = s, kj[x] = j, kr[x] = above;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kCand / kSelThreads; ++x)
-      if (kr[x] < K) cs[kr[x]] = ks[x], cj[kr[x]] = kj[x];
-    if (tid == 0) n_cand = min(n, K);
-    __syncthreads();
+  const float* sc = score + (size_t)local * sl.stride;
+  // ---- screen scores: piece r of a lane is blocks base + 128 r + 4 lane .. + 3, what lies behind `own` is kNone
+  auto piece = [&](int j) {
+    float4 v = make_float4(kNone, kNone, kNone, kNone);
+    if (j < own) v = *reinterpret_cast<const float4*>(sc + j);
+    if (j + 1 >= own) v.y = kNone;
+    if (j + 2 >= own) v.z = kNone;
+    if (j + 3 >= own) v.w = kNone;
+    return v;
   };
-  int scored = 0;
-  for (int base = 0; base < own; base += kSelThreads) {
-    const int j = base + tid;
-    const bool in = j < own && (sc[j] >= bar || odd);
-    const uint32_t m = __ballot_sync(~0u, in);
-    if (m) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&n_cand, __popc(m));
-      at = __shfl_sync(~0u, at, 0) + __popc(m & ((1u << lane) - 1));
-      if (in) cj[at] = j;
+  // the largest of this lane's subsets, and (rows of one batch) of its pieces
+  float mx[4] = {kNone, kNone, kNone, kNone}, pm[kHeld];
+  for (int base = 0; base < own; base += kHeld * 128) {
+    float4 v[kHeld];
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      const int j = base + 128 * r + 4 * lane;
+      if (base + 128 * r + 128 <= own) v[r] = *reinterpret_cast<const float4*>(sc + j);
+      else v[r] = piece(j);
     }
-    // room for one more round?  (uniform: decided from the shared count)
-    if (bar == -CUDART_INF_F || (base / kSelThreads) % 3 == 2) {
-      __syncthreads();
-      const int n = n_cand;
-      __syncthreads();
-      if (n > kCand - 3 * kSelThreads) {
-        keep_best(scored);
-        scored = n_cand;
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      mx[0] = fmaxf(mx[0], v[r].x), mx[1] = fmaxf(mx[1], v[r].y);
+      mx[2] = fmaxf(mx[2], v[r].z), mx[3] = fmaxf(mx[3], v[r].w);
+      pm[r] = fmaxf(fmaxf(v[r].x, v[r].y), fmaxf(v[r].z, v[r].w));
+    }
+  }
+  // ---- twice the error bound: 2 |q| max |hi| (2^-8 + 2^-10), and room for products below the normal range
+  float sq = 0.f, hm = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const float a = __uint_as_float(qw[i] << 16), b = __uint_as_float(qw[i] & 0xffff0000u);
+    sq = fmaf(a, a, fmaf(b, b, sq));
+  }
+  const int tile = sl.per_token ? (tok - sl.t0) * ((G + 15) / 16) + (h % G) / 16
+                                : tile_base(p, sl, row, G) + ((tok - clip(__ldg(p.cu + row), sl)) * G + h % G) / 16;
+  for (int i = lane; i * sl.chunk < own; i += 32) {
+    const float x = hmax[((size_t)tile * c.h_kv + head) * sl.nchunk + i];
+    hm = x > hm || x != x ? x : hm;  // NaN stays
+  }
+  for (int off = 16; off; off >>= 1) {
+    sq += __shfl_xor_sync(~0u, sq, off);
+    const float x = __shfl_xor_sync(~0u, hm, off);
+    hm = x > hm || x != x ? x : hm;
+  }
+  // |q . hi| and all its partial sums are at most this: up to 2^126 no screen score can be other than finite
+  const float size = sqrtf(sq) * sqrtf(hm);
+  const bool odd = !(size <= 8.5070592e37f);
+  const float e2 = 2.f * (size * 4.8828125e-3f + 1e-30f);
+  // K-th largest of the subsets' maxima (K < own, so as many subsets hold a block), from below; 64 subsets do for small K
+  float bar = -CUDART_INF_F;
+  if (!odd) {
+    uint32_t key[4];
+    if (K <= 20) {
+      key[0] = key_of(fmaxf(mx[0], mx[1])), key[1] = key_of(fmaxf(mx[2], mx[3]));
+      bar = own > 64 ? of_key(kth_key<2>(key, K)) - e2 : bar;
+    }
+    if (K > 20 || own <= 64) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) key[x] = key_of(mx[x]);
+      bar = of_key(kth_key<4>(key, K)) - e2;
+    }
+  }
+  // ---- candidates, in no order: pieces with one as bits, then those pieces once more
+  if (lane == 0) ls.count = 0;
+  __syncwarp();
+  if (!odd) {
+    auto add = [&](float s, int j) {
+      if (s >= bar) {
+        const int at = atomicAdd(&ls.count, 1);
+        if (at < kCand) ls.screen[at] = s, ls.j[at] = j;
+      }
+    };
+    for (int base = 0; base < own; base += kHeld * 128) {
+      uint32_t hit = 0;
+      if (own <= kHeld * 128) {
+#pragma unroll
+        for (int r = 0; r < kHeld; ++r) hit |= (uint32_t)(pm[r] >= bar) << r;
+      } else {
+#pragma unroll
+        for (int r = 0; r < kHeld; ++r) {
+          const float4 v = piece(base + 128 * r + 4 * lane);
+          hit |= (uint32_t)(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bar) << r;
+        }
+      }
+      while (hit) {
+        const int j = base + 128 * (__ffs(hit) - 1) + 4 * lane;
+        hit &= hit - 1;
+        const float4 v = piece(j);
+        add(v.x, j), add(v.y, j + 1), add(v.z, j + 2), add(v.w, j + 3);
       }
     }
+    __syncwarp();
   }
-  keep_best(scored);
-  const int n = n_cand;
-  if (tid < n) {
-    const int j = cj[tid];
-    int below = 0;
-    for (int i = 0; i < n; ++i) below += cj[i] < j;
-    out[below] = j;
+  int n = ls.count;
+  // picks: this lane's list positions lane + 32 x, as bits
+  uint32_t picks = 0;
+  if (odd || n > kCand) {
+    n = many_candidates<D>(c, row, head, qr, ls, sc, own, odd ? -CUDART_INF_F : bar, K);
+    for (int x = 0; x * 32 < n; ++x) {
+      const int i = x * 32 + lane;
+      if (i < n && among(ls, nullptr, n, K, ls.exact[i], ls.j[i])) picks |= 1u << x;
+    }
+  } else {
+    // Candidates more than 2 e above the K-th largest screen score are in; only the others have to be told apart.
+    uint32_t key[kCand / 32];
+#pragma unroll
+    for (int x = 0; x < kCand / 32; ++x) key[x] = x * 32 + lane < n ? key_of(ls.screen[x * 32 + lane]) : 0;
+    const uint32_t kth = n <= 64 ? kth_key<2>(key, K) : (n <= 128 ? kth_key<4>(key, K) : kth_key<kCand / 32>(key, K));
+    const float sure = of_key(kth | 0xffffu) + e2;
+    int n_sure = 0;
+    uint32_t is_sure = 0;
+#pragma unroll
+    for (int x = 0; x < kCand / 32; ++x)
+      if (x * 32 < n) {
+        const bool s = x * 32 + lane < n && of_key(key[x]) > sure;
+        is_sure |= (uint32_t)s << x;
+        n_sure += __popc(__ballot_sync(~0u, s));
+      }
+    const int m = rescore<D>(c, row, head, qr, ls, n, [&](int i) { return !(is_sure >> (i >> 5) & 1); });
+    picks = is_sure;
+    // the ones in doubt, two per lane, against all of them: by the upper words of their scores, where those decide
+    for (int first = 0; first < m; first += 64) {
+      int above[2] = {0, 0}, same[2] = {0, 0}, k2[2], w[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        k2[x] = first + 32 * x + lane;
+        w[x] = ls.page[min(k2[x], m - 1)];
+      }
+#pragma unroll 8
+      for (int k = 0; k < m; ++k) {
+        const int o = ls.page[k];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) above[x] += o > w[x], same[x] += o == w[x];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (k2[x] < m) {
+          const int i = ls.todo[k2[x]];
+          const bool in = same[x] == 1 ? above[x] < K - n_sure : among(ls, ls.todo, m, K - n_sure, ls.exact[i], ls.j[i]);
+          ls.screen[i] = in ? 1.f : 0.f;  // screen scores are done with
+        }
+    }
+    __syncwarp();
+    for (int x = 0; x * 32 < n; ++x) {
+      const int i = x * 32 + lane;
+      if (i < n && !(is_sure >> x & 1) && ls.screen[i] != 0.f) picks |= 1u << x;
+    }
   }
-  for (int i = n + tid; i < topk; i += kSelThreads) out[i] = i == n ? own : -1;
+  // ---- in ascending order
+  __syncwarp();
+  int k = 0;
+  for (int x = 0; x * 32 < n; ++x) {
+    const bool s = picks >> x & 1;
+    const uint32_t b = __ballot_sync(~0u, s);
+    if (s) ls.todo[k + __popc(b & ((1u << lane) - 1))] = ls.j[x * 32 + lane];
+    k += __popc(b);
+  }
+  __syncwarp();
+  for (int i = lane; i < topk; i += 32) {
+    if (i < k) {
+      const int j = ls.todo[i];
+      int below = 0;
+#pragma unroll 8
+      for (int y = 0; y < k; ++y) below += ls.todo[y] < j;
+      out[below] = j;
+    } else {
+      out[i] = i == k ? own : -1;
+    }
+  }
 }
 
 // Tiles of 16 rows, per KV head.
@@ -379,13 +558,14 @@ cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, i
     sl.chunk = chunk_of(c);
     sl.nchunk = (c.max_blocks + sl.chunk - 1) / sl.chunk;
     sl.stride = stride_of(c);
-    const dim3 g1((unsigned)tiles, c.h_kv, sl.nchunk), g2(sl.t1 - t0, h_q);
+    const dim3 g1((unsigned)tiles, c.h_kv, sl.nchunk);
+    const unsigned g2 = (unsigned)(((long long)(sl.t1 - t0) * h_q + kSelWarps - 1) / kSelWarps);
     if (c.d == 64) {
       score_kernel<64><<<g1, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
-      select_kernel<64><<<g2, kSelThreads, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
+      select_kernel<64><<<g2, kSelWarps * 32, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
     } else {
       score_kernel<128><<<g1, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
-      select_kernel<128><<<g2, kSelThreads, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
+      select_kernel<128><<<g2, kSelWarps * 32, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

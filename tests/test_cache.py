@@ -257,3 +257,92 @@ def test_chunks_of_many_tokens(hq, h, d, B, kind, n, scale):
     r = Run(2, 1400 // B + 4, 1100 // B + 8, hq, h, d, B, kind, 0, 4, seed=B + hq, scale=scale)
     for a in n:
         r.step([a, a // 2 + 1])
+
+
+def _route_alone(cent, q, own_tokens, B, topk, max_blocks=None, T_pad=0):
+    """cache_route on centroids given as float64 [blocks, h, d] (split into hi + lo here), one row whose last token is
+    the query's; returns sel [1, h_q, topk] and the centroids as held."""
+    nb, h, d = cent.shape
+    c = moba.alloc_cache(1, nb + 2, max_blocks or nb + 2, h, d, B)
+    hi = cent.float().to(torch.bfloat16)
+    lo = (cent.float() - hi.float()).to(torch.bfloat16)
+    c.cent[0, :nb], c.cent[1, :nb] = hi.cuda(), lo.cuda()
+    perm = torch.randperm(nb + 2, generator=torch.Generator().manual_seed(3))
+    c.cent[:] = torch.cat([c.cent[:, :nb], torch.zeros((2, 2, h, d), device="cuda", dtype=torch.bfloat16)], 1)[:, torch.argsort(perm)]
+    c.block_table[0, :nb + 1] = perm[:nb + 1].to(torch.int32).cuda()
+    c.row_state[0, 0], c.row_state[0, 1] = own_tokens + 1, own_tokens // B + 1
+    T = q.shape[0]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = moba.CachePlan(torch.tensor([0, T], **i32), torch.zeros(T, **i32), torch.full((T,), own_tokens, **i32),
+                          torch.zeros(T, **i32))
+    ws = c.alloc_workspace(T, q.shape[1])
+    sel = moba.cache_route(c, plan, q.cuda(), topk, workspace=ws)
+    assert moba.check_status(ws) == 0
+    return sel.cpu(), hi.double() + lo.double()
+
+
+def _route_exact(held, q, own, topk):
+    h = held.shape[1]
+    g = q.shape[1] // h
+    sel = torch.full(q.shape[:2] + (topk,), -1, dtype=torch.int32)
+    for t in range(q.shape[0]):
+        for i in range(q.shape[1]):
+            x = (held[:own, i // g] * q[t, i].double()).sum(-1)
+            x = torch.where(torch.isnan(x), float("-inf"), x)
+            got = sorted(torch.sort(x, descending=True, stable=True).indices[:topk - 1].tolist()) + [own]
+            sel[t, i, :len(got)] = torch.tensor(got, dtype=torch.int32)
+    return sel
+
+
+@gpu
+@pytest.mark.parametrize("topk", [2, 17, 64])
+@pytest.mark.parametrize("what", ["random", "all_equal", "few_values", "lo_decides", "huge", "inf_query", "nan_query",
+                                  "zero_query", "tiny"])
+def test_routing_ties_and_extremes(what, topk):
+    g = torch.Generator().manual_seed(topk)
+    nb, h, d, B, T = 1500, 2, 64, 16, 3
+    cent = torch.randn((nb, h, d), generator=g).double()
+    q = torch.randn((T, 4, d), generator=g).to(torch.bfloat16)
+    if what == "all_equal":                     # every block a candidate: the list overflows, ties go to lower blocks
+        cent[:] = cent[:1]
+    elif what == "few_values":                  # small integers: sums are exact, many ties
+        cent, q = torch.randint(-1, 2, (nb, h, d), generator=g).double(), torch.randint(-1, 2, (T, 4, d), generator=g).to(torch.bfloat16)
+    elif what == "lo_decides":                  # blocks that differ below bf16 only
+        cent = cent[:1] * (1 + torch.randint(-60, 60, (nb, 1, 1), generator=g).double() * 2.0 ** -16)
+    elif what == "huge":                        # 32-bit sums overflow, 64-bit ones do not
+        cent, q = cent * 1e25, (q.float() * 1e20).to(torch.bfloat16)
+    elif what == "inf_query":
+        q[1, 0, 3] = float("inf")
+    elif what == "nan_query":
+        q[1, 0, 3] = float("nan")
+    elif what == "zero_query":
+        q[:] = 0
+    elif what == "tiny":                        # products below the normal range of 32 bits
+        cent, q = cent * 1e-25, (q.float() * 1e-20).to(torch.bfloat16)
+    own = nb - 1
+    sel, held = _route_alone(cent, q, own * B + 5, B, topk)
+    assert torch.equal(sel, _route_exact(held, q, own, topk))
+
+
+@gpu
+@pytest.mark.parametrize("own", [0, 1, 3, 4, 5, 127, 128, 129, 255, 256, 257, 600])
+def test_routing_around_the_sizes_of_its_steps(own):
+    g = torch.Generator().manual_seed(own)
+    cent = torch.randn((own + 1, 1, 128), generator=g).double()
+    q = torch.randn((2, 3, 128), generator=g).to(torch.bfloat16)
+    for topk in (1, 5, 64):
+        sel, held = _route_alone(cent, q, own * 32, 32, topk, max_blocks=own + 7)
+        assert torch.equal(sel, _route_exact(held, q, own, topk)), topk
+
+
+@gpu
+def test_routing_in_slabs():
+    """More screen scores than the workspace holds at a time: the tokens go through in parts."""
+    g = torch.Generator().manual_seed(1)
+    cent = torch.randn((40, 1, 64), generator=g).double()
+    T, hq = 700, 24
+    q = torch.randn((T, hq, 64), generator=g).to(torch.bfloat16)
+    sel, held = _route_alone(cent, q, 39 * 16, 16, 6, max_blocks=9000)
+    x = torch.einsum("thd,jd->thj", q.double(), held[:39, 0])
+    want = torch.sort(x, dim=-1, descending=True, stable=True).indices[..., :5].sort(-1).values
+    assert torch.equal(sel[..., :5].long(), want) and (sel[..., 5] == 39).all()
