@@ -33,6 +33,8 @@ namespace moba {
 namespace cache {
 namespace {
 
+constexpr int kFewTokens = 4;  // see append_kernel
+
 struct RowInfo {
   int row, t_begin;  // the row's first new token
   int pos0;          // and its position
@@ -67,10 +69,21 @@ __device__ __forceinline__ uint4 raw_key(const View& c, const RowInfo& R, const 
                                          (((size_t)R.row * kHistRing + (pos & (kHistRing - 1))) * c.h_kv + head) * D + ch);
 }
 
-__device__ __noinline__ float conv_in_64(const float* x, const float* w, int W) {
+// One channel of k' in 64 bits: taps x0 .. x7 (zero from the width on), weights w[0, W).
+__device__ __noinline__ float conv_in_64(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                         const float* w, int W) {
+  const float x[kMaxWidth] = {x0, x1, x2, x3, x4, x5, x6, x7};
   double z = 0.0;
-  for (int l = 0; l < W; ++l) z += (double)w[l] * (double)x[l];
-  return (float)((double)x[0] + z / (1.0 + exp(-z)));
+#pragma unroll
+  for (int l = 0; l < kMaxWidth; ++l)
+    if (l < W) z += (double)__ldg(w + l) * (double)x[l];
+  return (float)((double)x0 + z / (1.0 + exp(-z)));
+}
+
+// Element e of 8 bf16.
+__device__ __forceinline__ float element(const uint4& u, int e) {
+  const uint32_t w = e < 2 ? u.x : (e < 4 ? u.y : (e < 6 ? u.z : u.w));
+  return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
 }
 
 // k' of 8 channels of token rel.
@@ -78,20 +91,26 @@ template <int D>
 __device__ __forceinline__ uint4 conv8(const View& c, const RowInfo& R, const bf16* k, const float* w, int head, int ch,
                                        int rel) {
   const int W = c.conv_width;
+  uint4 raw[kMaxWidth];
+#pragma unroll
+  for (int l = 0; l < kMaxWidth; ++l) raw[l] = l < W ? raw_key<D>(c, R, k, head, ch, rel - l) : make_uint4(0, 0, 0, 0);
   float x0[8], z[8], size[8];
+  bf16x8_to_f32(raw[0], x0);
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = size[e] = 0.f;
-  for (int l = 0; l < W; ++l) {
-    float x[8];
-    bf16x8_to_f32(raw_key<D>(c, R, k, head, ch, rel - l), x);
+  const float* wc = w + ((size_t)head * D + ch) * W;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float wl = __ldg(w + ((size_t)head * D + ch + e) * W + l);
-      if (l == 0) x0[e] = x[e];
-      z[e] = fmaf(wl, x[e], z[e]);
-      size[e] += fabsf(wl * x[e]);
+  for (int l = 0; l < kMaxWidth; ++l)
+    if (l < W) {
+      float x[8];
+      bf16x8_to_f32(raw[l], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float wl = __ldg(wc + e * W + l);
+        z[e] = fmaf(wl, x[e], z[e]);
+        size[e] += fabsf(wl * x[e]);
+      }
     }
-  }
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -100,16 +119,9 @@ __device__ __forceinline__ uint4 conv8(const View& c, const RowInfo& R, const bf
     const float E = 9.5367432e-7f * (fabsf(x0[e]) + size[e] * (1.2f + 0.25f * fminf(fabsf(z[e]), 88.f)));
     const uint16_t a = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] - E));
     const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] + E));
-    if (a != b || !(fabsf(z[e]) < 80.f)) {
-      float xs[kMaxWidth], ws[kMaxWidth];
-      for (int l = 0; l < W; ++l) {
-        float x[8];
-        bf16x8_to_f32(raw_key<D>(c, R, k, head, ch, rel - l), x);
-        xs[l] = x[e];
-        ws[l] = __ldg(w + ((size_t)head * D + ch + e) * W + l);
-      }
-      y[e] = conv_in_64(xs, ws, W);
-    }
+    if (a != b || !(fabsf(z[e]) < 80.f))
+      y[e] = conv_in_64(element(raw[0], e), element(raw[1], e), element(raw[2], e), element(raw[3], e), element(raw[4], e),
+                        element(raw[5], e), element(raw[6], e), element(raw[7], e), wc + e * W, W);
   }
   return f32_to_bf16x8(y);
 }
@@ -203,7 +215,7 @@ __device__ __forceinline__ float scale_of(float m) {
 }
 
 template <int KIND, int D, int BLK, bool CONV>
-__global__ void __launch_bounds__(Shape<D, BLK>::THREADS)
+__global__ void __launch_bounds__(Shape<D, BLK>::THREADS, 512 / Shape<D, BLK>::THREADS)
 append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict__ v, const float* __restrict__ w,
               int per_token, int heads_per_cta, int32_t* status) {
   using S = Shape<D, BLK>;
@@ -215,21 +227,24 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
   const int tid = threadIdx.x, u = blockIdx.x;
   const int head0 = blockIdx.y * heads_per_cta, head1 = min(c.h_kv, head0 + heads_per_cta);
   const int ch = tid % LANES * 8, off0 = tid / LANES * NCH;  // this thread's channels and first token of a block
-  const int total = min(__ldg(p.cu + c.rows), p.T);
-  // ---- which run
+  // ---- which run.  Loads that do not need one another's answers are made together.
   RowInfo R;
   int first_rel;  // its first token, relative to the row's first
+  int end, len, total;
   if (per_token) {
-    if (u >= total) return;
-    R.row = __ldg(p.row + u);
-    const int pos = __ldg(p.pos + u);
-    if ((unsigned)R.row >= (unsigned)c.rows) return;
-    R.t_begin = __ldg(p.cu + R.row);
+    const int row = __ldg(p.row + u), pos = __ldg(p.pos + u);
+    total = __ldg(p.cu + c.rows);
+    if ((unsigned)row >= (unsigned)c.rows) return;
+    R.row = row;
+    R.t_begin = __ldg(p.cu + row);
+    end = __ldg(p.cu + row + 1);
+    len = c.state[2 * row];
     first_rel = u - R.t_begin;
-    if (R.t_begin < 0 || first_rel < 0 || pos < first_rel) return;
+    if (R.t_begin < 0 || first_rel < 0 || pos < first_rel || u >= total) return;
     R.pos0 = pos - first_rel;
     if (first_rel > 0 && pos % B != 0) return;
   } else {
+    total = __ldg(p.cu + c.rows);
     int lo = 0, hi = c.rows;  // largest row with cu / B + 2 row <= u
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -237,15 +252,16 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     }
     R.row = lo;
     R.t_begin = __ldg(p.cu + lo);
-    if (R.t_begin < 0 || R.t_begin >= total) return;
+    end = __ldg(p.cu + lo + 1);
+    len = c.state[2 * lo];
+    if (R.t_begin < 0 || R.t_begin >= min(total, p.T)) return;
     R.pos0 = __ldg(p.pos + R.t_begin);
     if (R.pos0 < 0) return;
     const int i = u - (R.t_begin / B + 2 * lo);  // number of the block among the row's touched ones
     first_rel = i == 0 ? 0 : (R.pos0 / B + i) * B - R.pos0;
   }
-  R.n = min(__ldg(p.cu + R.row + 1), total) - R.t_begin;
+  R.n = min(end, min(total, p.T)) - R.t_begin;
   if (R.n <= 0 || first_rel >= R.n) return;
-  const int len = c.state[2 * R.row];
   if ((long long)R.pos0 + R.n != len || len > (long long)c.max_blocks * B) {
     if (tid == 0) set_status(status, kStatusBadTable);
     return;
@@ -263,6 +279,34 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
   }
   const bool has_old = R.pos0 % B != 0;
   bool bad = false;
+
+  if (R.n <= kFewTokens && R.n == n_first && R.len % B != 0) {
+    // A few tokens of an unfinished block (a generated token, mostly): one CTA for all heads, a thread group per
+    // (token, head).  With a CTA per head, one group in 16 would work.
+    if (blockIdx.y > 0) return;
+    for (int i = tid / LANES; i < R.n * c.h_kv; i += GROUPS) {
+      const int rel = i / c.h_kv, head = i % c.h_kv;
+      const size_t at = ((size_t)(R.t_begin + rel) * c.h_kv + head) * D + ch;
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(v + at));
+      uint4 x;
+      if constexpr (CONV) x = conv8<D>(c, R, k, w, head, ch, rel);
+      else x = raw_key<D>(c, R, k, head, ch, rel);
+      *tail_at<D>(c.tail_k, c, R.row, j0, head, R.pos0 % B + rel, ch) = finite8(x, &bad);
+      *tail_at<D>(c.tail_v, c, R.row, j0, head, R.pos0 % B + rel, ch) = finite8(y, &bad);
+    }
+    if constexpr (CONV) {
+      __syncthreads();  // the history has been read
+      const int m = min(R.n, Wm1);
+      for (int i = tid / LANES; i < m * c.h_kv; i += GROUPS) {
+        const int rel = R.n - m + i / c.h_kv, head = i % c.h_kv;
+        *reinterpret_cast<uint4*>(
+            c.hist + (((size_t)R.row * kHistRing + ((R.pos0 + rel) & (kHistRing - 1))) * c.h_kv + head) * D + ch) =
+            raw_key<D>(c, R, k, head, ch, rel);
+      }
+    }
+    if (bad) set_status(status, kStatusNonFinite);
+    return;
+  }
 
   for (int j = j0; j <= j1; ++j) {
     const int lo = max(R.pos0 - j * B, 0), hi = min(R.len - j * B, B);  // new tokens inside the block
@@ -296,18 +340,15 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     for (int head = head0; head < head1; ++head) {
       fetch(head + 1);
       uint4 x[NCH], y[NCH];
-      if constexpr (CONV) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i)
-          if (off0 + i >= lo && off0 + i < hi) x[i] = conv8<D>(c, R, k, w, head, ch, rel0 + off0 + i);
+      uint4* src = ring + ((head - head0) & 1) * S::STAGE + tid;
+      if constexpr (CONV) {  // the converted tokens go where copies of the others go
+        const int i1 = min(hi - off0, NCH);
+#pragma unroll 1
+        for (int i = max(lo - off0, 0); i < i1; ++i) src[i * THREADS] = conv8<D>(c, R, k, w, head, ch, rel0 + off0 + i);
       }
       cp_async_wait<1>();
-      const uint4* src = ring + ((head - head0) & 1) * S::STAGE + tid;
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        if (!CONV || off0 + i < lo || off0 + i >= hi) x[i] = src[i * THREADS];
-        y[i] = src[(NCH + i) * THREADS];
-      }
+      for (int i = 0; i < NCH; ++i) x[i] = src[i * THREADS], y[i] = src[(NCH + i) * THREADS];
       float mk = finite_amax<NCH>(x, &bad), mv = finite_amax<NCH>(y, &bad);
       if (keep) {
 #pragma unroll

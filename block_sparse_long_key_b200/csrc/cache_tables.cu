@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kScanThreads = 1024;
 constexpr int kFillThreads = 256;
+constexpr int kCuShared = 4096;  // rows whose first tokens fit shared memory
 
 struct Sums {
   long long tokens, need, gone;
@@ -56,8 +57,50 @@ __device__ Sums block_scan(Sums s, Sums* warp_sums) {
   return w ? s + warp_sums[w - 1] : s;
 }
 
+// Lists token t of `total` and enters its page in the block table where it is the page's first.
+__device__ __forceinline__ void fill_token(const View& c, const Plan& p, const RowPlan* rp, const int* cu, int t, int total,
+                                           int32_t* status) {
+  int row = -1, pos = -1, slot = -1;
+  if (t < total) {
+    int lo = 0, hi = c.rows;  // largest row whose tokens begin at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= t) lo = mid; else hi = mid;
+    }
+    row = lo;
+    const RowPlan q = rp[row];
+    if (q.flags & kRowServed) {
+      pos = q.length + t - cu[row];
+      const int lb = 31 - __clz(c.B), j = pos >> lb, off = pos & (c.B - 1);
+      int32_t* entry = c.table + (size_t)row * c.max_blocks + j;
+      int pg;
+      if (j < q.held) {
+        pg = *entry;
+      } else {
+        // from < n_pages and j - held < n_pages: one turn of the ring at most
+        long long at = (long long)q.from + (j - q.held);
+        if (at >= c.n_pages) at -= c.n_pages;
+        pg = c.free_pages[at];
+        if (off == 0) *entry = pg;
+      }
+      if ((unsigned)pg < (unsigned)c.n_pages) slot = pg * c.B + off;
+      else set_status(status, kStatusBadTable);
+    }
+  }
+  p.row[t] = row, p.pos[t] = pos, p.slot[t] = slot;
+}
+
+// Gives row r's pages back.
+__device__ __forceinline__ void release_row(const View& c, const RowPlan& q, int r, int tid, int nth) {
+  for (int i = tid; i < q.held; i += nth) {
+    long long at = (long long)q.from + i;
+    if (at >= c.n_pages) at -= c.n_pages;
+    if (at < c.n_pages) c.free_pages[at] = c.table[(size_t)r * c.max_blocks + i];
+  }
+}
+
 __global__ void __launch_bounds__(kScanThreads)
-scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_out, Plan p, RowPlan* rp,
+scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_out, Plan p, RowPlan* rp, int alone,
             int32_t* status) {
   __shared__ Sums warp_sums[32];
   __shared__ Sums carry;
@@ -133,39 +176,30 @@ scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_
     ring_out[0] = head + taken;
     ring_out[1] = tail + carry.gone;
   }
+  if (!alone) return;
+  // small steps end here, without a second launch (the loop's last barrier has published rp and cu)
+  const int total = (int)min(carry.tokens, (long long)p.T);
+  for (int t = tid; t < p.T; t += kScanThreads) fill_token(c, p, rp, p.cu, t, total, status);
+  for (int r = tid >> 5; r < c.rows; r += kScanThreads / 32) {
+    const RowPlan q = rp[r];
+    if (q.flags & kRowRelease) release_row(c, q, r, tid & 31, 32);
+  }
 }
 
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(View c, Plan p, const RowPlan* rp, int32_t* status) {
+  __shared__ int cu[kCuShared];
+  const bool here = c.rows <= kCuShared;
+  if (here) {
+    for (int i = threadIdx.x; i < c.rows; i += kFillThreads) cu[i] = __ldg(p.cu + i);
+    __syncthreads();
+  }
   const int nth = gridDim.x * kFillThreads;
   const int total = __ldg(p.cu + c.rows);
-  for (long long i = blockIdx.x * kFillThreads + threadIdx.x; i < p.T; i += nth) {
-    const int t = (int)i;
-    int row = -1, pos = -1, slot = -1;
-    if (t < total) {
-      row = upper_seq(p.cu, c.rows, t);
-      const RowPlan q = rp[row];
-      if (q.flags & kRowServed) {
-        pos = q.length + t - __ldg(p.cu + row);
-        const int j = pos / c.B;
-        int32_t* entry = c.table + (size_t)row * c.max_blocks + j;
-        int pg;
-        if (j < q.held) {
-          pg = *entry;
-        } else {
-          pg = c.free_pages[((long long)q.from + j - q.held) % c.n_pages];
-          if (pos % c.B == 0) *entry = pg;
-        }
-        if ((unsigned)pg < (unsigned)c.n_pages) slot = pg * c.B + pos % c.B;
-        else set_status(status, kStatusBadTable);
-      }
-    }
-    p.row[t] = row, p.pos[t] = pos, p.slot[t] = slot;
-  }
+  for (long long t = blockIdx.x * kFillThreads + threadIdx.x; t < p.T; t += nth)
+    fill_token(c, p, rp, here ? cu : p.cu, (int)t, total, status);
   for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
     const RowPlan q = rp[r];
-    if (!(q.flags & kRowRelease)) continue;
-    for (int i = threadIdx.x; i < q.held; i += kFillThreads)
-      c.free_pages[((long long)q.from + i) % c.n_pages] = c.table[(size_t)r * c.max_blocks + i];
+    if (q.flags & kRowRelease) release_row(c, q, r, threadIdx.x, kFillThreads);
   }
 }
 
@@ -199,9 +233,11 @@ cudaError_t launch_reset(const View& c, cudaStream_t st) {
 
 cudaError_t launch_tables(const View& c, const int32_t* new_len, int32_t* state_out, long long* ring_out,
                           const Plan& p, RowPlan* rp, int32_t* status, cudaStream_t st) {
-  scan_kernel<<<1, kScanThreads, 0, st>>>(c, new_len, state_out, ring_out, p, rp, status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // One CTA lists up to two tokens per thread about as fast as a second launch starts.
+  const int alone = p.T <= 2 * kScanThreads && c.rows <= kScanThreads;
+  scan_kernel<<<1, kScanThreads, 0, st>>>(c, new_len, state_out, ring_out, p, rp, alone, status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || alone) return e;
   const int work = p.T > c.rows ? p.T : c.rows;
   const int grid = (work + kFillThreads - 1) / kFillThreads;
   fill_kernel<<<grid < 1184 ? grid : 1184, kFillThreads, 0, st>>>(c, p, rp, status);

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from typing import NamedTuple, Optional, Tuple
+from typing import Optional, Tuple
 
 import torch
 
@@ -325,12 +325,29 @@ CACHE_KINDS = {"e4m3": (0, torch.float8_e4m3fn), "int8": (1, torch.int8)}
 _CACHE_HIST = 16
 
 
-class CachePlan(NamedTuple):
-    """The new tokens of a step (see moba_cache_plan), packed row after row."""
-    cu_new: torch.Tensor     # int32 [rows + 1]
-    token_row: torch.Tensor  # int32 [T]
-    token_pos: torch.Tensor  # int32 [T]
-    slot_map: torch.Tensor   # int32 [T]
+class CachePlan:
+    """The new tokens of a step (see moba_cache_plan), packed row after row: cu_new int32 [rows + 1], token_row,
+    token_pos, slot_map int32 [T].  Checked once; the tensors are fixed."""
+    __slots__ = ("cu_new", "token_row", "token_pos", "slot_map", "total_new", "rows", "index", "struct", "_ref")
+
+    def __init__(self, cu_new, token_row, token_pos, slot_map):
+        _need(cu_new, torch.int32, "cu_new", 1)
+        T = token_row.shape[0]
+        for n, t in (("token_row", token_row), ("token_pos", token_pos), ("slot_map", slot_map)):
+            _need_shape(t, torch.int32, n, (T,))
+        if len({t.get_device() for t in (cu_new, token_row, token_pos, slot_map)}) != 1:
+            raise ValueError("a plan's tensors must be on one device")
+        self._set(cu_new, token_row, token_pos, slot_map, T)
+
+    def _set(self, cu_new, token_row, token_pos, slot_map, T):
+        self.cu_new, self.token_row, self.token_pos, self.slot_map = cu_new, token_row, token_pos, slot_map
+        self.total_new, self.rows, self.index = T, cu_new.shape[0] - 1, cu_new.get_device()
+        self.struct = PlanStruct(T, cu_new.data_ptr(), token_row.data_ptr(), token_pos.data_ptr(), slot_map.data_ptr())
+        self._ref = ctypes.byref(self.struct)
+        return self
+
+    def __iter__(self):
+        return iter((self.cu_new, self.token_row, self.token_pos, self.slot_map))
 
 
 class Cache:
@@ -368,6 +385,7 @@ class Cache:
         self.rows, self.n_pages, self.max_blocks, self.h_kv = int(rows), int(n_pages), int(max_blocks), int(h_kv)
         self.head_dim, self.block_size, self.kind, self.conv_width = int(d), int(B), kind, int(conv_width)
         self.device = devs.pop()
+        self.index = self.device.index
         for n, x in given.items():
             setattr(self, n, x)
         self.struct = CacheStruct(self.rows, self.n_pages, self.max_blocks, self.h_kv, self.head_dim, self.block_size,
@@ -382,40 +400,45 @@ class Cache:
 
     def reset(self) -> None:
         """Empties the cache (moba_cache_reset)."""
-        with _on(self.device):
-            _check(lib().moba_cache_reset(self._ref, _stream_of(self.device)), "moba_cache_reset")
+        _launch(self, "moba_cache_reset")
 
 
-class _Here:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+# The current stream's handle: torch.cuda.current_stream builds a Stream object, which takes longer than the rest of a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-_HERE = _Here()
-
-
-def _on(device):
-    """Makes `device` the current one for a launch."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _stream_of(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _need_shape(t, dtype, name, shape):
+    """A contiguous CUDA tensor of this type and shape (one look where all is well: these calls are short)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _need(t, dtype, name)
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _same_device(cache, **tensors):
     for n, t in tensors.items():
-        if t is not None and t.device != cache.device:
+        if t is not None and t.get_device() != cache.index:
             raise ValueError("%s is on %s, the cache on %s" % (n, t.device, cache.device))
 
 
-def _need_shape(t, dtype, name, shape):
-    _need(t, dtype, name)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+def _launch(cache, name, *args):
+    """Calls moba_<name>(cache, *args, stream) on the cache's device and its current stream."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == cache.index:
+        rc = fn(cache._ref, *args, _raw_stream(cache.index))
+    else:
+        with torch.cuda.device(cache.device):
+            rc = fn(cache._ref, *args, _raw_stream(cache.index))
+    if rc != MOBA_OK:
+        raise MobaError(rc, name)
+
+
+def _check_plan(cache, plan):
+    if not isinstance(plan, CachePlan):
+        raise TypeError("plan must be a CachePlan")
+    if plan.rows != cache.rows or plan.index != cache.index:
+        raise ValueError("the plan is for %d rows on device %d, the cache has %d on %d"
+                         % (plan.rows, plan.index, cache.rows, cache.index))
 
 
 def alloc_cache(rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: int, block_size: int,
@@ -442,40 +465,33 @@ def alloc_cache(rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: i
     return c
 
 
-def _plan_struct(cache, plan: CachePlan, total_new: int):
-    _need_shape(plan.cu_new, torch.int32, "plan.cu_new", (cache.rows + 1,))
-    for n, t in (("token_row", plan.token_row), ("token_pos", plan.token_pos), ("slot_map", plan.slot_map)):
-        _need_shape(t, torch.int32, "plan." + n, (total_new,))
-        _same_device(cache, **{"plan." + n: t})
-    _same_device(cache, **{"plan.cu_new": plan.cu_new})
-    return PlanStruct(total_new, plan.cu_new.data_ptr(), plan.token_row.data_ptr(), plan.token_pos.data_ptr(),
-                      plan.slot_map.data_ptr())
-
-
 def cache_tables(cache: Cache, new_len: torch.Tensor, total_new: int, row_state_out=None, ring_out=None,
                  plan: Optional[CachePlan] = None, workspace=None) -> CachePlan:
     """Pages and slots for ``new_len`` (int32 [rows]; -1 releases a row) new tokens, at most ``total_new`` in all
     (moba_cache_tables).  Advances the cache's row_state and ring, or writes the state after the step to
-    ``row_state_out`` / ``ring_out``.  Returns the plan the other calls take."""
+    ``row_state_out`` / ``ring_out``.  Returns the plan the other calls take (written into ``plan`` if given)."""
     _need_shape(new_len, torch.int32, "new_len", (cache.rows,))
-    total_new = int(total_new)
-    if total_new < 0:
+    T, dev = int(total_new), cache.device
+    if T < 0:
         raise ValueError("total_new must not be negative")
     if row_state_out is not None:
         _need_shape(row_state_out, torch.int32, "row_state_out", (cache.rows, 2))
     if ring_out is not None:
         _need_shape(ring_out, torch.int64, "ring_out", (2,))
-    dev = cache.device
     if plan is None:
-        plan = CachePlan(torch.empty(cache.rows + 1, dtype=torch.int32, device=dev),
-                         *(torch.empty(total_new, dtype=torch.int32, device=dev) for _ in range(3)))
+        # one allocation, its parts 16-byte aligned
+        a, b = (cache.rows + 4) & ~3, (T + 3) & ~3
+        cu, _, row, _, pos, _, slot, _ = torch.empty(a + 3 * b, dtype=torch.int32, device=dev).split_with_sizes(
+            (cache.rows + 1, a - cache.rows - 1, T, b - T, T, b - T, T, b - T))
+        plan = CachePlan.__new__(CachePlan)._set(cu, row, pos, slot, T)
+    else:
+        _check_plan(cache, plan)
+        if plan.total_new != T:
+            raise ValueError("the plan has room for %d tokens, not total_new = %d" % (plan.total_new, T))
     ws = cache.alloc_workspace(0) if workspace is None else workspace
     _same_device(cache, new_len=new_len, row_state_out=row_state_out, ring_out=ring_out, workspace=ws)
-    ps = _plan_struct(cache, plan, total_new)
-    with _on(dev):
-        rc = lib().moba_cache_tables(cache._ref, new_len.data_ptr(), _addr(row_state_out), _addr(ring_out),
-                                     ctypes.byref(ps), ws.data_ptr(), ws.numel(), _stream_of(dev))
-    _check(rc, "moba_cache_tables")
+    _launch(cache, "moba_cache_tables", new_len.data_ptr(), _addr(row_state_out), _addr(ring_out), plan._ref,
+            ws.data_ptr(), ws.numel())
     return plan
 
 
@@ -486,8 +502,8 @@ def _addr(t: Optional[torch.Tensor]):
 def cache_append(cache: Cache, plan: CachePlan, k: torch.Tensor, v: torch.Tensor, conv_w=None, workspace=None) -> None:
     """Writes the new keys and values [T, h_kv, d] bf16 into the cache, through the key conv when the cache has one
     (``conv_w`` fp32 [h_kv, d, conv_width]) (moba_cache_append)."""
-    T = plan.token_row.shape[0]
-    shape = (T, cache.h_kv, cache.head_dim)
+    _check_plan(cache, plan)
+    shape = (plan.total_new, cache.h_kv, cache.head_dim)
     _need_shape(k, torch.bfloat16, "k", shape)
     _need_shape(v, torch.bfloat16, "v", shape)
     if (conv_w is not None) != (cache.conv_width > 0):
@@ -496,29 +512,29 @@ def cache_append(cache: Cache, plan: CachePlan, k: torch.Tensor, v: torch.Tensor
         _need_shape(conv_w, torch.float32, "conv_w", (cache.h_kv, cache.head_dim, cache.conv_width))
     ws = alloc_workspace(256, cache.device) if workspace is None else workspace
     _same_device(cache, k=k, v=v, conv_w=conv_w, workspace=ws)
-    ps = _plan_struct(cache, plan, T)
-    with _on(cache.device):
-        rc = lib().moba_cache_append(cache._ref, ctypes.byref(ps), k.data_ptr(), v.data_ptr(), _addr(conv_w),
-                                     ws.data_ptr(), ws.numel(), _stream_of(cache.device))
-    _check(rc, "moba_cache_append")
+    _launch(cache, "moba_cache_append", plan._ref, k.data_ptr(), v.data_ptr(), _addr(conv_w), ws.data_ptr(), ws.numel())
+
+
+def _check_q(cache, plan, q):
+    _check_plan(cache, plan)
+    _need(q, torch.bfloat16, "q", 3)
+    T, h_q, d = q.shape
+    if T != plan.total_new or d != cache.head_dim:
+        raise ValueError("q must have shape (%d, h_q, %d), got %s" % (plan.total_new, cache.head_dim, tuple(q.shape)))
+    return T, h_q
 
 
 def cache_route(cache: Cache, plan: CachePlan, q: torch.Tensor, topk: int, workspace=None, sel_idx=None) -> torch.Tensor:
     """The blocks of every new query: sel_idx int32 [T, h_q, topk] (moba_cache_route)."""
-    T = plan.token_row.shape[0]
-    _need(q, torch.bfloat16, "q", 3)
-    h_q = q.shape[1]
-    _need_shape(q, torch.bfloat16, "q", (T, h_q, cache.head_dim))
+    T, h_q = _check_q(cache, plan, q)
+    topk = int(topk)
     if sel_idx is None:
         sel_idx = torch.empty((T, h_q, topk), dtype=torch.int32, device=cache.device)
-    _need_shape(sel_idx, torch.int32, "sel_idx", (T, h_q, topk))
+    else:
+        _need_shape(sel_idx, torch.int32, "sel_idx", (T, h_q, topk))
     ws = cache.alloc_workspace(T, h_q) if workspace is None else workspace
     _same_device(cache, q=q, sel_idx=sel_idx, workspace=ws)
-    ps = _plan_struct(cache, plan, T)
-    with _on(cache.device):
-        rc = lib().moba_cache_route(cache._ref, ctypes.byref(ps), q.data_ptr(), h_q, int(topk), sel_idx.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream_of(cache.device))
-    _check(rc, "moba_cache_route")
+    _launch(cache, "moba_cache_route", plan._ref, q.data_ptr(), h_q, topk, sel_idx.data_ptr(), ws.data_ptr(), ws.numel())
     return sel_idx
 
 
@@ -526,25 +542,22 @@ def cache_attention(cache: Cache, plan: CachePlan, q: torch.Tensor, sel_idx: Opt
                     workspace=None, out=None, lse=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Attention of the new queries over the blocks of ``sel_idx`` (cache_route's), or over all earlier tokens when it
     is None.  Returns (out bf16 [T, h_q, d], lse fp32 [T, h_q]) (moba_cache_attention)."""
-    T = plan.token_row.shape[0]
-    _need(q, torch.bfloat16, "q", 3)
-    h_q = q.shape[1]
-    _need_shape(q, torch.bfloat16, "q", (T, h_q, cache.head_dim))
+    T, h_q = _check_q(cache, plan, q)
     topk = 1
     if sel_idx is not None:
         _need(sel_idx, torch.int32, "sel_idx", 3)
         topk = sel_idx.shape[2]
         _need_shape(sel_idx, torch.int32, "sel_idx", (T, h_q, topk))
-    dev = cache.device
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((T, h_q), dtype=torch.float32, device=dev) if lse is None else lse
-    _need_shape(out, torch.bfloat16, "out", tuple(q.shape))
-    _need_shape(lse, torch.float32, "lse", (T, h_q))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need_shape(out, torch.bfloat16, "out", q.shape)
+    if lse is None:
+        lse = torch.empty((T, h_q), dtype=torch.float32, device=cache.device)
+    else:
+        _need_shape(lse, torch.float32, "lse", (T, h_q))
     ws = cache.alloc_workspace(T, h_q) if workspace is None else workspace
     _same_device(cache, q=q, sel_idx=sel_idx, out=out, lse=lse, workspace=ws)
-    ps = _plan_struct(cache, plan, T)
-    with _on(dev):
-        rc = lib().moba_cache_attention(cache._ref, ctypes.byref(ps), q.data_ptr(), h_q, _addr(sel_idx), topk,
-                                        out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_of(dev))
-    _check(rc, "moba_cache_attention")
+    _launch(cache, "moba_cache_attention", plan._ref, q.data_ptr(), h_q, _addr(sel_idx), topk, out.data_ptr(),
+            lse.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse
