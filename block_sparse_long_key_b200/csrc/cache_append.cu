@@ -23,8 +23,8 @@
 // fp32, then bf16) of the value summed in 64 bits: it is formed in 32 bits
 // first, with a bound E on its error, and again in 64 bits only where a bf16
 // rounding boundary lies within E (about one element in a thousand).  A
-// block's sum is kept in 64 bits, where sums of bf16 values are exact unless
-// their exponents span more than 2^38.
+// block's sum is that of its threads' sums (of at most 8 tokens, in 32 bits)
+// in 64 bits, in a fixed order.
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
@@ -170,9 +170,16 @@ struct Shape {
   static constexpr int LANES = D / 8;               // threads across a token
   static constexpr int GROUPS = THREADS / LANES;    // token groups of NCH consecutive tokens
   static constexpr int STAGE = 2 * NCH * THREADS;   // 16-byte slots of one head's K and V
-  static constexpr int BYTES = 2 * STAGE * 16 + THREADS * 8 * 8;
+  static constexpr int BYTES = 2 * STAGE * 16 + THREADS * 8 * 4;
   static_assert(NCH * GROUPS == BLK, "tile");
 };
+
+// Where the sum of channel 8 ck + e of a token group is kept: 8 rows of D / 8 values, rotated so that both the threads
+// that hold 8 channels each and those that take one channel each meet every bank once.
+template <int D>
+__device__ __forceinline__ int sum_place(int ck, int e) {
+  return e * (D / 8) + ((ck + (D == 128 ? 2 * e : e)) & (D / 8 - 1));
+}
 
 template <int NCH>
 __device__ __forceinline__ float amax8(const uint4* x) {
@@ -215,14 +222,14 @@ __device__ __forceinline__ float scale_of(float m) {
 }
 
 template <int KIND, int D, int BLK, bool CONV>
-__global__ void __launch_bounds__(Shape<D, BLK>::THREADS, 512 / Shape<D, BLK>::THREADS)
+__global__ void __launch_bounds__(Shape<D, BLK>::THREADS, (CONV || Shape<D, BLK>::NCH > 4 ? 512 : 768) / Shape<D, BLK>::THREADS)
 append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict__ v, const float* __restrict__ w,
               int per_token, int heads_per_cta, int32_t* status) {
   using S = Shape<D, BLK>;
   constexpr int THREADS = S::THREADS, NCH = S::NCH, LANES = S::LANES, GROUPS = S::GROUPS, B = BLK;
   extern __shared__ __align__(16) unsigned char smem[];
   uint4* ring = reinterpret_cast<uint4*>(smem);                            // [2][K, V][NCH][THREADS]
-  double* gsum = reinterpret_cast<double*>(smem + 2 * S::STAGE * 16);      // [GROUPS][8][LANES]
+  float* gsum = reinterpret_cast<float*>(smem + 2 * S::STAGE * 16);        // [GROUPS][D], swizzled
   __shared__ float red[2][THREADS / 32];
   const int tid = threadIdx.x, u = blockIdx.x;
   const int head0 = blockIdx.y * heads_per_cta, head1 = min(c.h_kv, head0 + heads_per_cta);
@@ -365,20 +372,17 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         mv = fmaxf(mv, __shfl_xor_sync(~0u, mv, off));
       }
       if ((tid & 31) == 0) red[0][tid >> 5] = mk, red[1][tid >> 5] = mv;
-      {
-        double s[8];
+      float s[8];  // of this thread's tokens: exact unless their exponents span more than 2^13
+      bf16x8_to_f32(x[0], s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = 0.0;
+      for (int i = 1; i < NCH; ++i) {
+        float f[8];
+        bf16x8_to_f32(x[i], f);
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          float f[8];
-          bf16x8_to_f32(x[i], f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[e] += (double)f[e];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gsum[(tid / LANES * 8 + e) * LANES + tid % LANES] = s[e];
+        for (int e = 0; e < 8; ++e) s[e] += f[e];
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) gsum[off0 / NCH * D + sum_place<D>(tid % LANES, e)] = s[e];
       __syncthreads();
       mk = red[0][0], mv = red[1][0];
 #pragma unroll
@@ -391,7 +395,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
       if (tid < D) {
         double t = 0.0;
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) t += gsum[(g * 8 + (tid & 7)) * LANES + tid / 8];
+        for (int g = 0; g < GROUPS; ++g) t += (double)gsum[g * D + sum_place<D>(tid >> 3, tid & 7)];
         const float mean = (float)(t * (1.0 / B));
         const bf16 hi16 = __float2bfloat16_rn(mean);
         c.cent[at * D + tid] = hi16;

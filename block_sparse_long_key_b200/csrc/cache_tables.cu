@@ -11,7 +11,7 @@
 //
 // Kernel one scans the rows in one CTA and writes the state after the step
 // (it is the only one to read the state before, so both may be one buffer);
-// kernel two lists the tokens, one thread per token.  A page is first used by
+// kernel two lists the tokens, four per thread.  A page is first used by
 // the token at its start (pages are taken only for blocks without tokens), so
 // that token's thread writes the block table entry.
 #include "cache.cuh"
@@ -57,37 +57,64 @@ __device__ Sums block_scan(Sums s, Sums* warp_sums) {
   return w ? s + warp_sums[w - 1] : s;
 }
 
-// Lists token t of `total` and enters its page in the block table where it is the page's first.
-__device__ __forceinline__ void fill_token(const View& c, const Plan& p, const RowPlan* rp, const int* cu, int t, int total,
-                                           int32_t* status) {
-  int row = -1, pos = -1, slot = -1;
-  if (t < total) {
-    int lo = 0, hi = c.rows;  // largest row whose tokens begin at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cu[mid] <= t) lo = mid; else hi = mid;
+// Lists the tokens 4 i .. 4 i + 3 (of `total`; the arrays end at T) and enters the pages whose first token is among
+// them in the block table.
+__device__ __forceinline__ void fill_tokens(const View& c, const Plan& p, const RowPlan* rp, const int* cu, int i, int total,
+                                            int32_t* status) {
+  const int lb = 31 - __clz(c.B), first = 4 * i;
+  int out[3][4];
+  int lo = 0, hi = c.rows;  // largest row whose tokens begin at or before `first`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= first) lo = mid; else hi = mid;
+  }
+  int row = lo - 1, begin = 0, end = first, block = -1, page = -1;  // the row of the last token, its tokens, its last page
+  RowPlan q{0, 0, 0, 0};
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int t = first + x;
+    out[0][x] = out[1][x] = out[2][x] = -1;
+    if (t >= total) continue;
+    while (t >= end && row + 1 < c.rows) {
+      ++row;
+      begin = cu[row];
+      end = row + 1 < c.rows ? cu[row + 1] : total;
+      if (t < end) q = rp[row], block = -1;
     }
-    row = lo;
-    const RowPlan q = rp[row];
-    if (q.flags & kRowServed) {
-      pos = q.length + t - cu[row];
-      const int lb = 31 - __clz(c.B), j = pos >> lb, off = pos & (c.B - 1);
+    out[0][x] = row;
+    if (!(q.flags & kRowServed)) continue;
+    const int pos = q.length + t - begin, j = pos >> lb, off = pos & (c.B - 1);
+    if (j != block || off == 0) {
       int32_t* entry = c.table + (size_t)row * c.max_blocks + j;
-      int pg;
       if (j < q.held) {
-        pg = *entry;
+        page = *entry;
       } else {
         // from < n_pages and j - held < n_pages: one turn of the ring at most
         long long at = (long long)q.from + (j - q.held);
         if (at >= c.n_pages) at -= c.n_pages;
-        pg = c.free_pages[at];
-        if (off == 0) *entry = pg;
+        page = c.free_pages[at];
+        if (off == 0) *entry = page;
       }
-      if ((unsigned)pg < (unsigned)c.n_pages) slot = pg * c.B + off;
-      else set_status(status, kStatusBadTable);
+      block = j;
+      if ((unsigned)page >= (unsigned)c.n_pages) {
+        set_status(status, kStatusBadTable);
+        page = -1;
+      }
+    }
+    out[1][x] = pos;
+    if (page >= 0) out[2][x] = page * c.B + off;
+  }
+  int32_t* dst[3] = {p.row, p.pos, p.slot};
+#pragma unroll
+  for (int y = 0; y < 3; ++y) {
+    if (first + 4 <= p.T) {
+      *reinterpret_cast<int4*>(dst[y] + first) = make_int4(out[y][0], out[y][1], out[y][2], out[y][3]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (first + x < p.T) dst[y][first + x] = out[y][x];
     }
   }
-  p.row[t] = row, p.pos[t] = pos, p.slot[t] = slot;
 }
 
 // Gives row r's pages back.
@@ -104,7 +131,7 @@ scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_
             int32_t* status) {
   __shared__ Sums warp_sums[32];
   __shared__ Sums carry;
-  __shared__ long long taken;
+  __shared__ unsigned long long taken;
   const int tid = threadIdx.x;
   long long head = c.ring[0], tail = c.ring[1];
   const bool ring_ok = head >= 0 && tail >= head && tail - head <= c.n_pages;
@@ -141,6 +168,7 @@ scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_
       if (n < 0) s.gone = held;
     }
     const Sums mine = s;
+    int got = 0;  // pages this row takes
     s = block_scan(s, warp_sums) + carry;
     if (r < c.rows) {
       if (mine.need > 0 && s.need > avail) {
@@ -162,24 +190,26 @@ scan_kernel(View c, const int32_t* new_len, int32_t* state_out, long long* ring_
         state_out[2 * r] = 0, state_out[2 * r + 1] = 0;
       } else if (ok) {
         state_out[2 * r] = L + n, state_out[2 * r + 1] = held + (int)mine.need;
-        if (mine.need) atomicAdd(reinterpret_cast<unsigned long long*>(&taken), (unsigned long long)mine.need);
+        got = (int)mine.need;
       } else {
         state_out[2 * r] = c.state[2 * r], state_out[2 * r + 1] = c.state[2 * r + 1];
       }
     }
+    got = __reduce_add_sync(~0u, got);
+    if ((tid & 31) == 0 && got) atomicAdd(&taken, (unsigned long long)got);
     __syncthreads();
     if (tid == kScanThreads - 1) carry = s;
     __syncthreads();
   }
   if (tid == 0) {
     if (carry.gone > c.n_pages - avail) atomicOr(status, kStatusBadTable);
-    ring_out[0] = head + taken;
+    ring_out[0] = head + (long long)taken;
     ring_out[1] = tail + carry.gone;
   }
   if (!alone) return;
   // small steps end here, without a second launch (the loop's last barrier has published rp and cu)
   const int total = (int)min(carry.tokens, (long long)p.T);
-  for (int t = tid; t < p.T; t += kScanThreads) fill_token(c, p, rp, p.cu, t, total, status);
+  for (int i = tid; i < (p.T + 3) / 4; i += kScanThreads) fill_tokens(c, p, rp, p.cu, i, total, status);
   for (int r = tid >> 5; r < c.rows; r += kScanThreads / 32) {
     const RowPlan q = rp[r];
     if (q.flags & kRowRelease) release_row(c, q, r, tid & 31, 32);
@@ -195,8 +225,9 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(View c, Plan p, cons
   }
   const int nth = gridDim.x * kFillThreads;
   const int total = __ldg(p.cu + c.rows);
-  for (long long t = blockIdx.x * kFillThreads + threadIdx.x; t < p.T; t += nth)
-    fill_token(c, p, rp, here ? cu : p.cu, (int)t, total, status);
+  const int n4 = p.T / 4 + (p.T % 4 != 0);
+  for (int i = blockIdx.x * kFillThreads + threadIdx.x; i < n4; i += nth)
+    fill_tokens(c, p, rp, here ? cu : p.cu, i, total, status);
   for (int r = blockIdx.x; r < c.rows; r += gridDim.x) {
     const RowPlan q = rp[r];
     if (q.flags & kRowRelease) release_row(c, q, r, threadIdx.x, kFillThreads);
@@ -233,12 +264,12 @@ cudaError_t launch_reset(const View& c, cudaStream_t st) {
 
 cudaError_t launch_tables(const View& c, const int32_t* new_len, int32_t* state_out, long long* ring_out,
                           const Plan& p, RowPlan* rp, int32_t* status, cudaStream_t st) {
-  // One CTA lists up to two tokens per thread about as fast as a second launch starts.
-  const int alone = p.T <= 2 * kScanThreads && c.rows <= kScanThreads;
+  // One CTA lists up to four tokens per thread in less time than a second launch takes.
+  const int alone = p.T <= 4 * kScanThreads && c.rows <= kScanThreads;
   scan_kernel<<<1, kScanThreads, 0, st>>>(c, new_len, state_out, ring_out, p, rp, alone, status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || alone) return e;
-  const int work = p.T > c.rows ? p.T : c.rows;
+  const int work = p.T / 4 + 1 > c.rows ? p.T / 4 + 1 : c.rows;
   const int grid = (work + kFillThreads - 1) / kFillThreads;
   fill_kernel<<<grid < 1184 ? grid : 1184, kFillThreads, 0, st>>>(c, p, rp, status);
   return cudaGetLastError();

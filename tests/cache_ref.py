@@ -20,6 +20,7 @@ class RefCache:
     def __init__(self, rows, n_pages, max_blocks, h_kv, d, B, kind, conv_width):
         self.rows, self.n_pages, self.max_blocks, self.h, self.d, self.B = rows, n_pages, max_blocks, h_kv, d, B
         self.kind, self.W = kind, conv_width
+        self.cents = {}   # page -> centroids as the cache under test holds them, where routing is to follow those
         self.free = deque(range(n_pages))
         self.pages = [[] for _ in range(rows)]
         self.length = [0] * rows
@@ -123,8 +124,8 @@ class RefCache:
                 continue
             r, own = row[t], pos[t] // self.B
             if r not in cents:
-                cs = [self.centroid(r, j) for j in range(self.length[r] // self.B)]
-                cents[r] = torch.stack([a.double() + b.double() for a, b in cs]) if cs else None
+                cs = [self.cents.get(self.pages[r][j]) for j in range(self.length[r] // self.B)]
+                cents[r] = torch.stack(cs) if cs else None
             for h in range(hq):
                 got = []
                 if own:
