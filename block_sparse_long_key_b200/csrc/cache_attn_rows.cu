@@ -2,21 +2,20 @@
 // a prompt): the arithmetic of cache_attn.cu on tcgen05.
 //
 // A CTA takes 128 query rows ((token, group member) of one request and KV
-// head; row = TMEM lane = softmax thread) and walks key tiles of 128 positions.
+// head; row = TMEM lane = softmax thread) and walks key tiles of 64 positions.
 //   producers (4 warps)  8-bit pages -> fp16 K and V tiles in shared memory
-//                        (128-byte swizzle); the partial block's bf16 goes the
-//                        same way under a power of two that keeps every bit
-//   softmax (4 warps)    S from TMEM, weights back into the columns of S as fp16;
-//                        one of their threads issues the products,
-//                        S = Q K^T (M = N = 128, K = d) and O += P V (N = d, K = 128)
-// S and O take 256 TMEM columns and the tiles 96 KB (d = 128), so two CTAs
-// share an SM and one's products run under the other's exponentials.  The
-// reference of a row moves only when its maximum grows by more than 2^8, so O
-// (in TMEM) is seldom rescaled: weights are 2^(x - m + 7) <= 2^15.
+//                        (128-byte swizzle, two of each); the partial block's
+//                        bf16 goes the same way under a power of two that
+//                        keeps every bit
+//   products (1 thread)  S = Q K^T (M = 128, N = 64, K = d) into one of two
+//                        TMEM tiles, O += P V (N = d, K = 64)
+//   softmax (4 warps)    S from TMEM, weights back into its columns as fp16
+// The scores of tile i + 1 are formed while the softmax is at tile i, so the
+// softmax warps wait for nobody in the steady state.  S and O take 256 TMEM
+// columns and the tiles 96 KB (d = 128): two CTAs share an SM.  The reference
+// of a row moves only when its maximum grows by more than 2^8, so O (in TMEM)
+// is seldom rescaled: weights are 2^(x - m + 7) <= 2^15.
 //
-// Both the exponentials (128 x 128 per tile, 16 per clock and SM) and the
-// products (2 x 128 x 128 x d) come to about 1000 clocks per tile and SM at
-// d = 128; the conversion of a tile is 128 threads x 2 d pieces beside them.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
@@ -29,24 +28,26 @@ namespace cache {
 namespace {
 
 constexpr int kRows = 128;      // query rows per CTA
-constexpr int kKeys = 128;      // key positions per tile
-constexpr int kUnits = 8;       // units of 16 positions per tile
-constexpr int kThreads = 256;   // 4 softmax warps, 4 producer warps
+constexpr int kKeys = 64;       // key positions per tile
+constexpr int kUnits = 4;       // units of 16 positions per tile, one per producer warp
+constexpr int kThreads = 288;   // 4 softmax warps, 4 producer warps, 1 warp for the products
 constexpr float kOffset = 7.f;
 constexpr float kSlack = 8.f;   // growth of a row's maximum that leaves its reference alone
 
 template <int D>
 struct Layout {
   static constexpr int KB = D / 64;
-  static constexpr uint32_t REGION = 128 * 128;  // 128 rows of 64 fp16
-  static constexpr uint32_t Q_OFF = 0, K_OFF = KB * REGION, V_OFF = 2 * KB * REGION;
-  static constexpr uint32_t UNIT_OFF = 3 * KB * REGION;         // float4 [2][8]: ks, lv, rest, 2^-7 / vs
+  static constexpr uint32_t Q_REGION = 128 * 128;              // 128 rows of 64 fp16
+  static constexpr uint32_t REGION = kKeys * 128;              // 64 keys of 64 fp16
+  static constexpr uint32_t TILE = KB * REGION;
+  static constexpr uint32_t Q_OFF = 0, K_OFF = KB * Q_REGION, V_OFF = K_OFF + 2 * TILE;
+  static constexpr uint32_t UNIT_OFF = V_OFF + 2 * TILE;       // float4 [2][kUnits]: ks, log2 vs, rest, 2^-7 / vs
   static constexpr uint32_t RED_OFF = UNIT_OFF + 2 * kUnits * 16;
-  static constexpr uint32_t MB_OFF = RED_OFF + 64;              // K full, V full, S, P, O
-  static constexpr uint32_t HOLD_OFF = MB_OFF + 40;
+  static constexpr uint32_t MB_OFF = RED_OFF + 64;             // K full, V full, S full, P full, O done: two each
+  static constexpr uint32_t HOLD_OFF = MB_OFF + 80;
   static constexpr uint32_t FAIL_OFF = HOLD_OFF + 4;
   static constexpr uint32_t BYTES = FAIL_OFF + 16 + 1024;
-  static constexpr uint32_t TM_S = 0, TM_O = 128, TMEM_COLS = 256;
+  static constexpr uint32_t TM_S = 0, TM_O = 2 * kKeys, TMEM_COLS = 256;
 };
 
 // Instruction descriptor: fp16 operands, fp32 sums.
@@ -98,6 +99,16 @@ __device__ __forceinline__ bool wait(uint32_t addr, uint32_t parity, uint64_t li
       else if (now - t0 > limit_ns) return false;
     }
   }
+}
+
+// 32 lanes x 16 consecutive columns: thread t of the warp writes its lane's.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 // Two fp32 at a time.
@@ -153,7 +164,9 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   const uint32_t sbase = smem_u32(sm);
-  const uint32_t mb_k = sbase + Ly::MB_OFF, mb_v = mb_k + 8, mb_s = mb_k + 16, mb_p = mb_k + 24, mb_o = mb_k + 32;
+  // barriers of tile i: the one of its parity, whose phase is i / 2
+  const uint32_t mb_k = sbase + Ly::MB_OFF, mb_v = mb_k + 16, mb_s = mb_k + 32, mb_p = mb_k + 48, mb_o = mb_k + 64;
+  auto got = [&](uint32_t mb, int i) { return wait(mb + 8 * (i & 1), (i >> 1) & 1); };
   volatile int* fail = reinterpret_cast<volatile int*>(sm + Ly::FAIL_OFF);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lb = 31 - __clz(c.B);
@@ -186,11 +199,14 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const int tail0 = (long long)(own + 1) * c.B > len ? own * c.B : 0x7fffffff;  // first position read from the tail
 
   if (tid == 0) {
-    tc::mbar_init(mb_k, 4);
-    tc::mbar_init(mb_v, 4);
-    tc::mbar_init(mb_s, 1);
-    tc::mbar_init(mb_p, 4);
-    tc::mbar_init(mb_o, 1);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(mb_k + 8 * x, 4);
+      tc::mbar_init(mb_v + 8 * x, 4);
+      tc::mbar_init(mb_s + 8 * x, 1);
+      tc::mbar_init(mb_p + 8 * x, 4);
+      tc::mbar_init(mb_o + 8 * x, 1);
+    }
     tc::mbar_init_fence();
     *fail = 0;
   }
@@ -201,24 +217,23 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   int pos = -1;
   size_t item = 0;
   if (warp < 4) {
-    uint4 x[D / 8];
     float m = 0.f;
     if (tid < rows) {
       pos = pos_of(tid);
       if (split == 0 && pos != __ldg(p.pos + t0 + (r0 + tid) / G)) set_status(status, kStatusBadTable);
       item = (size_t)(t0 + (r0 + tid) / G) * h_q + head * G + (r0 + tid) % G;
     }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      x[i] = tid < rows ? __ldg(reinterpret_cast<const uint4*>(q + item * D) + i) : make_uint4(0, 0, 0, 0);
-      m = amax8(x[i], m);
-    }
+    auto piece = [&](int i) {
+      return tid < rows ? __ldg(reinterpret_cast<const uint4*>(q + item * D) + i) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) m = amax8(piece(i), m);
     const int e = exponent(m);
     const float up = pow2f(8 - e);
     fac = pow2f(e - 8) * (kLog2e * rsqrtf((float)D));
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < D / 8; ++i)
-      *reinterpret_cast<uint4*>(sm + Ly::Q_OFF + (i / 8) * Ly::REGION + tc::sw128_offset(tid, i % 8)) = scale8(x[i], up);
+      *reinterpret_cast<uint4*>(sm + Ly::Q_OFF + (i / 8) * Ly::Q_REGION + tc::sw128_offset(tid, i % 8)) = scale8(piece(i), up);
     tc::fence_proxy_async();
   }
   tc::fence_before_sync();
@@ -228,7 +243,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
   float m = -CUDART_INF_F, l = 0.f;
 
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 8) {
     // =============================================================== producers
     const int pw = warp - 4;
     int tail_e[2] = {0, 0};
@@ -252,38 +267,34 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       for (int z = 0; z < 2; ++z)
         tail_e[z] = exponent(fmaxf(fmaxf(red[4 * z], red[4 * z + 1]), fmaxf(red[4 * z + 2], red[4 * z + 3])));
     }
-    // This warp's units of a tile: 2 pw, 2 pw + 1.  Piece z of a unit: 16 codes a lane, of row 8 (z / KB) + lane / 4 and
-    // the channels 64 (z % KB) + 16 (lane % 4) on; 8 lanes then store two rows' 64 bytes, every bank once.
+    // This warp's unit of a tile is pw.  Piece z: 16 codes a lane, of row 8 (z / KB) + lane / 4 and the channels
+    // 64 (z % KB) + 16 (lane % 4) on; 8 lanes then store two rows' 64 bytes, every bank once.
     constexpr int NP = D / 32;
     const int rr = lane >> 2, cq = lane & 3;
     const uint32_t code_at = rr * D + cq * 16;
     const uint32_t put_a = rr * 128 + ((2 * cq ^ rr) << 4), put_b = rr * 128 + (((2 * cq + 1) ^ rr) << 4);
-    auto unit_pos = [&](int i, int x) { return (kt0 + i) * kKeys + (2 * pw + x) * 16; };
+    auto unit_pos = [&](int i) { return (kt0 + i) * kKeys + pw * 16; };
     // A unit's table entry (only loaded here: nothing waits for it), and what it says: page; -1: zeros; -2: tail.
-    auto unit_entry = [&](int i, int x) {
-      const int ps = unit_pos(i, x);
+    auto unit_entry = [&](int i) {
+      const int ps = unit_pos(i);
       return i < nt && ps < kend && ps < tail0 ? __ldg(c.table + (size_t)row * c.max_blocks + (ps >> lb)) : 0;
     };
-    auto unit_page = [&](int entry, int i, int x) {
-      const int ps = unit_pos(i, x);
+    auto unit_page = [&](int entry, int i) {
+      const int ps = unit_pos(i);
       if (i >= nt || ps >= kend) return -1;
       if (ps >= tail0) return -2;
       if ((unsigned)entry < (unsigned)c.n_pages) return entry;
       set_status(status, kStatusBadTable);
       return -1;
     };
-    // address of a unit's codes inside the pages
-    auto unit_at = [&](int pg, int i, int x) {
-      return ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i, x) & (c.B - 1)) * D + code_at;
-    };
-    auto put = [&](uint32_t base, int x, int z, uint4 a, uint4 b) {
-      unsigned char* dst = sm + base + (z % Ly::KB) * Ly::REGION + (2 * (2 * pw + x) + z / Ly::KB) * 1024;
+    auto put = [&](uint32_t base, int z, uint4 a, uint4 b) {
+      unsigned char* dst = sm + base + (z % Ly::KB) * Ly::REGION + (2 * pw + z / Ly::KB) * 1024;
       *reinterpret_cast<uint4*>(dst + put_a) = a;
       *reinterpret_cast<uint4*>(dst + put_b) = b;
     };
-    auto put_tail = [&](uint32_t base, const bf16* tail, int i, int x, float up) {
+    auto put_tail = [&](uint32_t base, const bf16* tail, int i, float up) {
       const size_t at = (((size_t)row * 2 + (own & 1)) * c.h_kv + head) * c.B * D;
-      const int first = unit_pos(i, x) - tail0, n = mp + 1 - tail0;
+      const int first = unit_pos(i) - tail0, n = mp + 1 - tail0;
 #pragma unroll 1
       for (int z = 0; z < NP; ++z) {
         const int r = first + 8 * (z / Ly::KB) + rr;
@@ -292,142 +303,139 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
           const uint4* src = reinterpret_cast<const uint4*>(tail + at + (size_t)r * D + 64 * (z % Ly::KB) + 16 * cq);
           a = scale8(src[0], up), b = scale8(src[1], up);
         }
-        put(base, x, z, a, b);
+        put(base, z, a, b);
       }
     };
     // Registers hold one tile's pieces; a tile's are asked for as soon as the ones before have been stored.
-    uint4 kr[2][NP], vr[2][NP];
-    float sc[2] = {0.f, 1.f};  // lanes 0, 1: this lane's unit's scales
-    auto ask = [&](uint4 (*r)[NP], const uint8_t* base, const int* pg, int i) {
+    uint4 kr[NP], vr[NP];
+    float sc[2] = {0.f, 1.f};  // the unit's scales
+    auto ask = [&](uint4* r, const uint8_t* base, int pg, int i) {
+      const size_t at = pg >= 0 ? ((size_t)pg * c.h_kv + head) * c.B * D + (size_t)(unit_pos(i) & (c.B - 1)) * D + code_at : 0;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const size_t at = pg[x] >= 0 ? unit_at(pg[x], i, x) : 0;
-#pragma unroll
-        for (int z = 0; z < NP; ++z) {
-          r[x][z] = make_uint4(0, 0, 0, 0);
-          if (pg[x] >= 0) r[x][z] = __ldg(reinterpret_cast<const uint4*>(base + at + (z / Ly::KB) * 8 * D + (z % Ly::KB) * 64));
-        }
+      for (int z = 0; z < NP; ++z) {
+        r[z] = make_uint4(0, 0, 0, 0);
+        if (pg >= 0) r[z] = __ldg(reinterpret_cast<const uint4*>(base + at + (z / Ly::KB) * 8 * D + (z % Ly::KB) * 64));
       }
     };
-    auto ask_scales = [&](const int* pg) {
-      const int g = lane ? pg[1] : pg[0];
-      if (lane < 2 && g >= 0) {
-        const size_t at = (size_t)g * c.h_kv + head;
+    auto ask_scales = [&](int pg) {
+      if (pg >= 0) {
+        const size_t at = (size_t)pg * c.h_kv + head;
         sc[0] = __ldg(c.k_scale + at), sc[1] = __ldg(c.v_scale + at);
       }
     };
-    int pg[2] = {unit_page(unit_entry(0, 0), 0, 0), unit_page(unit_entry(0, 1), 0, 1)};
-    int next[2] = {unit_entry(1, 0), unit_entry(1, 1)};
+    int pg = unit_page(unit_entry(0), 0), next = unit_entry(1);
     ask(kr, c.k, pg, 0);
     ask(vr, c.v, pg, 0);
     ask_scales(pg);
     for (int i = 0; i < nt; ++i) {
-      // K tile free: the products of tile i - 1's scores are done
-      if (!__all_sync(~0u, i == 0 || wait(mb_s, (i - 1) & 1)) || *fail) { *fail = 1; break; }
-      if (lane < 2) {
-        const int g = lane ? pg[1] : pg[0];
-        const float ks = g >= 0 ? sc[0] : (g == -2 ? pow2f(tail_e[0] - 14) : 0.f);
-        const float vs = g >= 0 ? sc[1] : (g == -2 ? pow2f(tail_e[1] - 14) : 1.f);
+      const uint32_t k_tile = Ly::K_OFF + (i & 1) * Ly::TILE, v_tile = Ly::V_OFF + (i & 1) * Ly::TILE;
+      // K tile free: the scores of tile i - 2 are done
+      if (!__all_sync(~0u, i < 2 || got(mb_s, i - 2)) || *fail) { *fail = 1; break; }
+      if (pg == -2) {
+        put_tail(k_tile, c.tail_k, i, pow2f(14 - tail_e[0]));
+      } else {
+#pragma unroll
+        for (int z = 0; z < NP; ++z) {
+          uint4 a, b;
+          widen16<KIND>(kr[z], a, b);
+          put(k_tile, z, a, b);
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(mb_k + 8 * (i & 1));
+      const float ks = pg >= 0 ? sc[0] : (pg == -2 ? pow2f(tail_e[0] - 14) : 0.f);
+      const float vs = pg >= 0 ? sc[1] : (pg == -2 ? pow2f(tail_e[1] - 14) : 1.f);
+      const int now = pg;
+      pg = unit_page(next, i + 1);
+      next = unit_entry(i + 2);
+      ask(kr, c.k, pg, i + 1);
+      ask_scales(pg);
+      // V tile (and the unit's scales) free: the product of tile i - 2 is done, so its weights are, too
+      if (!__all_sync(~0u, i < 2 || got(mb_o, i - 2)) || *fail) { *fail = 1; break; }
+      if (lane == 0) {
         const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
-        *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + 2 * pw + lane) * 16) =
-            make_float4(ks, g == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);  // nothing: weights 0
+        *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + pw) * 16) =
+            make_float4(ks, now == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);  // nothing: weights 0
       }
+      if (now == -2) {
+        put_tail(v_tile, c.tail_v, i, pow2f(14 - tail_e[1]));
+      } else {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (pg[x] == -2) {
-          put_tail(Ly::K_OFF, c.tail_k, i, x, pow2f(14 - tail_e[0]));
-        } else {
-#pragma unroll
-          for (int z = 0; z < NP; ++z) {
-            uint4 a, b;
-            widen16<KIND>(kr[x][z], a, b);
-            put(Ly::K_OFF, x, z, a, b);
-          }
+        for (int z = 0; z < NP; ++z) {
+          uint4 a, b;
+          widen16<KIND>(vr[z], a, b);
+          put(v_tile, z, a, b);
         }
       }
       tc::fence_proxy_async();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(mb_k);
-      const int ng[2] = {unit_page(next[0], i + 1, 0), unit_page(next[1], i + 1, 1)};
-      next[0] = unit_entry(i + 2, 0), next[1] = unit_entry(i + 2, 1);
-      ask(kr, c.k, ng, i + 1);
-      ask_scales(ng);
-      // V tile free
-      if (!__all_sync(~0u, i == 0 || wait(mb_o, (i - 1) & 1)) || *fail) { *fail = 1; break; }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (pg[x] == -2) {
-          put_tail(Ly::V_OFF, c.tail_v, i, x, pow2f(14 - tail_e[1]));
-        } else {
-#pragma unroll
-          for (int z = 0; z < NP; ++z) {
-            uint4 a, b;
-            widen16<KIND>(vr[x][z], a, b);
-            put(Ly::V_OFF, x, z, a, b);
-          }
-        }
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(mb_v);
-      pg[0] = ng[0], pg[1] = ng[1];
+      if (lane == 0) tc::mbar_arrive(mb_v + 8 * (i & 1));
       ask(vr, c.v, pg, i + 1);
     }
+  } else if (warp == 8) {
+    // =============================================================== products
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_f16(kRows, kKeys, 0), id_o = idesc_f16(kRows, D, 1);
+      auto scores = [&](int i) {
+        tc::fence_after_sync();
+        const uint32_t k_tile = sbase + Ly::K_OFF + (i & 1) * Ly::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_bf16_ss(tmem + Ly::TM_S + (i & 1) * kKeys,
+                          tc::smem_desc(sbase + Ly::Q_OFF + (kk >> 2) * Ly::Q_REGION + (kk & 3) * 32, 16, 1024, tc::kLayoutSW128),
+                          tc::smem_desc(k_tile + (kk >> 2) * Ly::REGION + (kk & 3) * 32, 16, 1024, tc::kLayoutSW128), id_s,
+                          kk > 0);
+        tc::mma_commit(mb_s + 8 * (i & 1));
+      };
+      bool ok = nt == 0 || got(mb_k, 0);
+      if (nt > 0 && ok) scores(0);
+      for (int i = 0; ok && i < nt; ++i) {
+        if (i + 1 < nt) {  // the next scores go where the weights of tile i - 1 were: its product must be done
+          ok = got(mb_k, i + 1) && (i == 0 || got(mb_o, i - 1)) && !*fail;
+          if (!ok) break;
+          scores(i + 1);
+        }
+        ok = got(mb_v, i) && got(mb_p, i) && !*fail;
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t v_tile = sbase + Ly::V_OFF + (i & 1) * Ly::TILE;
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc::mma_bf16_ts(tmem + Ly::TM_O, tmem + Ly::TM_S + (i & 1) * kKeys + kk * 8,
+                          tc::smem_desc(v_tile + kk * 2048, Ly::REGION, 1024, tc::kLayoutSW128), id_o, i > 0 || kk > 0);
+        tc::mma_commit(mb_o + 8 * (i & 1));
+      }
+      if (!ok) *fail = 1;
+    }
+    __syncwarp();
   } else {
     // =============================================================== softmax
-    constexpr uint32_t id_s = idesc_f16(kRows, kKeys, 0), id_o = idesc_f16(kRows, D, 1);
     for (int i = 0; i < nt; ++i) {
-      bool got = true;
-      if (tid == 0) {
-        // the weights of the tile before, which these scores overwrite, have been read
-        got = (i == 0 || wait(mb_o, (i - 1) & 1)) && wait(mb_k, i & 1);
-        if (got) {
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk >> 2) * Ly::REGION + (kk & 3) * 32;
-            tc::mma_bf16_ss(tmem + Ly::TM_S, tc::smem_desc(sbase + Ly::Q_OFF + o, 16, 1024, tc::kLayoutSW128),
-                            tc::smem_desc(sbase + Ly::K_OFF + o, 16, 1024, tc::kLayoutSW128), id_s, kk > 0);
-          }
-          tc::mma_commit(mb_s);
-        }
-      }
-      __syncwarp();
-      got = got && wait(mb_s, i & 1);
-      if (!__all_sync(~0u, got) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, got(mb_s, i)) || *fail) { *fail = 1; break; }
       tc::fence_after_sync();
+      const uint32_t tm_s = tmem + lane_base + Ly::TM_S + (i & 1) * kKeys;
       const float4* prm = reinterpret_cast<const float4*>(sm + Ly::UNIT_OFF + (i & 1) * kUnits * 16);
       const int nvis = min(kKeys, min(pos + 1, kend) - (kt0 + i) * kKeys);  // visible keys of this row, from the first
-      if (!__all_sync(~0u, nvis == kKeys)) {  // hidden scores become -infinity where they are
-#pragma unroll 1
-        for (int h = 0; h < kKeys / 32; ++h) {
-          uint32_t s[32];
-          tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 32, s);
-          tc::tmem_ld_wait();
+      uint32_t s[2][32];  // scores; from its start on, pairs of weights take their place
+      tc::tmem_ld32(tm_s, s[0]);
+      tc::tmem_ld32(tm_s + 32, s[1]);
+      tc::tmem_ld_wait();
+      if (!__all_sync(~0u, nvis == kKeys)) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (32 * h + x >= nvis) s[x] = 0xff800000u;
-          tc::tmem_st32(tmem + lane_base + Ly::TM_S + h * 32, s);
-        }
-        tc::tmem_st_wait();
+        for (int x = 0; x < kKeys; ++x)
+          if (x >= nvis) s[x / 32][x % 32] = 0xff800000u;
       }
       float top[kUnits];  // largest score of each unit
 #pragma unroll
-      for (int h = 0; h < kKeys / 64; ++h) {
-        uint32_t s[2][32];
-        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 64, s[0]);
-        tc::tmem_ld32(tmem + lane_base + Ly::TM_S + h * 64 + 32, s[1]);
-        tc::tmem_ld_wait();
+      for (int u = 0; u < kUnits; ++u) {
+        float t = __uint_as_float(s[u / 2][16 * (u & 1)]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float t = __uint_as_float(s[u / 2][16 * (u & 1)]);
-#pragma unroll
-          for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[u / 2][16 * (u & 1) + x]));
-          top[4 * h + u] = t;
-        }
+        for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[u / 2][16 * (u & 1) + x]));
+        top[u] = t;
       }
-      // The units' scales: published with the V tile (whose barrier, unlike the K tile's, cannot get ahead of this warp).
-      if (!__all_sync(~0u, wait(mb_v, i & 1))) { *fail = 1; break; }
+      // the units' scales come with the V tile
+      if (!__all_sync(~0u, got(mb_v, i))) { *fail = 1; break; }
       float mx = -CUDART_INF_F;
       bool odd = false;  // a V scale below 2^-100
 #pragma unroll
@@ -443,108 +451,87 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         if (up) m = mx;
         l *= a;
         if (i > 0) {
+          if (!__all_sync(~0u, got(mb_o, i - 1))) { *fail = 1; break; }
+          tc::fence_after_sync();
 #pragma unroll 1
-          for (int h = 0; h < D / 32; ++h) {
-            uint32_t o[32];
-            tc::tmem_ld32(tmem + lane_base + Ly::TM_O + h * 32, o);
+          for (int h = 0; h < D / 16; ++h) {
+            uint32_t o[16];
+            tc::tmem_ld16(tmem + lane_base + Ly::TM_O + h * 16, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
-            tc::tmem_st32(tmem + lane_base + Ly::TM_O + h * 32, o);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * a);
+            tmem_st16(tmem + lane_base + Ly::TM_O + h * 16, o);
           }
         }
       }
       const float off = kOffset - (m == -CUDART_INF_F ? 0.f : m);
 #pragma unroll
-      for (int hp = 0; hp < 2; ++hp) {
-        uint32_t w[32];
+      for (int u = 0; u < kUnits; ++u) {
+        const float4 pr = prm[u];
+        const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f), b1 = pr.y + off;
+        const uint64_t f = pair(f1, f1), b = pair(b1, b1);
+        uint64_t sum = 0;  // two zeros
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[32];
-          tc::tmem_ld32(tmem + lane_base + Ly::TM_S + (2 * hp + h) * 32, s);
-          tc::tmem_ld_wait();
+        for (int x = 0; x < 16; x += 2) {
+          float e0, e1;
+          const uint32_t* z = &s[u / 2][16 * (u & 1) + x];
+          unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), f, b), e0, e1);
+          e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+          sum = add2(sum, pair(e0, e1));
+          s[0][8 * u + x / 2] = pack_f16(e0, e1);
+        }
+        float s0, s1;
+        unpair(sum, s0, s1);
+        l = fmaf(s0 + s1, pr.w, l);
+        if (odd) {
+          const __half2 z = __float2half2_rn(pr.z);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float4 pr = prm[2 * (2 * hp + h) + u];
-            const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f), b1 = pr.y + off;
-            const uint64_t f = pair(f1, f1), b = pair(b1, b1);
-            uint64_t sum = 0;  // two zeros
-#pragma unroll
-            for (int x = 0; x < 16; x += 2) {
-              float e0, e1;
-              unpair(fma2(pair(__uint_as_float(s[16 * u + x]), __uint_as_float(s[16 * u + x + 1])), f, b), e0, e1);
-              e0 = fast_exp2(e0), e1 = fast_exp2(e1);
-              sum = add2(sum, pair(e0, e1));
-              w[16 * h + 8 * u + x / 2] = pack_f16(e0, e1);
-            }
-            float s0, s1;
-            unpair(sum, s0, s1);
-            l = fmaf(s0 + s1, pr.w, l);
-            if (odd) {
-              const __half2 z = __float2half2_rn(pr.z);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[16 * h + 8 * u + x]), z);
-                w[16 * h + 8 * u + x] = *reinterpret_cast<const uint32_t*>(&y);
-              }
-            }
+          for (int x = 0; x < 8; ++x) {
+            __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][8 * u + x]), z);
+            s[0][8 * u + x] = *reinterpret_cast<const uint32_t*>(&y);
           }
         }
-        tc::tmem_st32(tmem + lane_base + Ly::TM_S + hp * 32, w);
       }
+      tc::tmem_st32(tm_s, s[0]);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(mb_p);
-      got = true;
-      if (tid == 0) {
-        got = wait(mb_p, i & 1);
-        if (got) {
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_bf16_ts(tmem + Ly::TM_O, tmem + Ly::TM_S + kk * 8,
-                            tc::smem_desc(sbase + Ly::V_OFF + kk * 2048, Ly::REGION, 1024, tc::kLayoutSW128), id_o,
-                            i > 0 || kk > 0);
-          tc::mma_commit(mb_o);
-        }
-      }
-      if (!__all_sync(~0u, got)) { *fail = 1; break; }
+      if (lane == 0) tc::mbar_arrive(mb_p + 8 * (i & 1));
     }
     // ---- result
-    bool got = nt == 0 || wait(mb_o, (nt - 1) & 1);
-    got = __all_sync(~0u, got) && !*fail;
-    if (!got) *fail = 1;
+    bool fine = nt == 0 || got(mb_o, nt - 1);
+    fine = __all_sync(~0u, fine) && !*fail;
+    if (!fine) *fail = 1;
     tc::fence_after_sync();
-    if (got) {
+    if (fine) {
       const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
-#pragma unroll
-      for (int h = 0; h < D / 32; ++h) {
-        uint32_t o[32];
+#pragma unroll 1
+      for (int h = 0; h < D / 16; ++h) {
+        uint32_t o[16];
         if (nt > 0) {
-          tc::tmem_ld32(tmem + lane_base + Ly::TM_O + h * 32, o);
+          tc::tmem_ld16(tmem + lane_base + Ly::TM_O + h * 16, o);
           tc::tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0;
+          for (int x = 0; x < 16; ++x) o[x] = 0;
         }
         if (tid < rows) {
           if (nsplit == 1) {
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
+            for (int x = 0; x < 16; x += 8) {
               uint4 y;
               uint32_t* yy = &y.x;
 #pragma unroll
               for (int z = 0; z < 4; ++z)
                 yy[z] = pack_bf16(l == 0.f ? 0.f : __uint_as_float(o[x + 2 * z]) * inv,
                                   l == 0.f ? 0.f : __uint_as_float(o[x + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + item * D + h * 32 + x) = y;
+              *reinterpret_cast<uint4*>(out + item * D + h * 16 + x) = y;
             }
           } else {
             float* b = part + (item * nsplit + split) * (D + 4);
 #pragma unroll
-            for (int x = 0; x < 32; x += 4)  // in units of cache_attn.cu's weights, 2^15
-              *reinterpret_cast<float4*>(b + h * 32 + x) =
+            for (int x = 0; x < 16; x += 4)  // in units of cache_attn.cu's weights, 2^15
+              *reinterpret_cast<float4*>(b + h * 16 + x) =
                   make_float4(__uint_as_float(o[x]) * 256.f, __uint_as_float(o[x + 1]) * 256.f,
                               __uint_as_float(o[x + 2]) * 256.f, __uint_as_float(o[x + 3]) * 256.f);
           }
@@ -565,10 +552,10 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   if (*fail) {
     // A completion never arrived: record it and give what is in flight a bounded chance to drain.
     if (tid == 0) set_status(status, kStatusTimeout);
-    wait(mb_s, 0, 50000000ull);
-    wait(mb_s, 1, 50000000ull);
-    wait(mb_o, 0, 50000000ull);
-    wait(mb_o, 1, 50000000ull);
+    for (int x = 0; x < 4; ++x) {
+      wait(mb_s + 8 * (x & 1), x >> 1, 50000000ull);
+      wait(mb_o + 8 * (x & 1), x >> 1, 50000000ull);
+    }
     __syncthreads();
   }
   if (warp == 4) {
