@@ -156,7 +156,8 @@ __device__ __forceinline__ float amax8(uint4 x, float m) {
   return m;
 }
 
-template <int D, int KIND>
+// ONE: blocks of at least a key tile, so that a tile has one pair of scales.
+template <int D, int KIND, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_blocks, int nsplit,
                  bf16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int32_t* status) {
@@ -330,7 +331,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     for (int i = 0; i < nt; ++i) {
       const uint32_t k_tile = Ly::K_OFF + (i & 1) * Ly::TILE, v_tile = Ly::V_OFF + (i & 1) * Ly::TILE;
       // K tile free: the scores of tile i - 2 are done
-      if (!__all_sync(~0u, i < 2 || got(mb_s, i - 2)) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, i < 2 || got(mb_s, i - 2))) { *fail = 1; break; }
       if (pg == -2) {
         put_tail(k_tile, c.tail_k, i, pow2f(14 - tail_e[0]));
       } else {
@@ -352,7 +353,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       ask(kr, c.k, pg, i + 1);
       ask_scales(pg);
       // V tile (and the unit's scales) free: the product of tile i - 2 is done, so its weights are, too
-      if (!__all_sync(~0u, i < 2 || got(mb_o, i - 2)) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, i < 2 || got(mb_o, i - 2))) { *fail = 1; break; }
       if (lane == 0) {
         const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
         *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + pw) * 16) =
@@ -392,11 +393,11 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       if (nt > 0 && ok) scores(0);
       for (int i = 0; ok && i < nt; ++i) {
         if (i + 1 < nt) {  // the next scores go where the weights of tile i - 1 were: its product must be done
-          ok = got(mb_k, i + 1) && (i == 0 || got(mb_o, i - 1)) && !*fail;
+          ok = got(mb_k, i + 1) && (i == 0 || got(mb_o, i - 1)) ;
           if (!ok) break;
           scores(i + 1);
         }
-        ok = got(mb_v, i) && got(mb_p, i) && !*fail;
+        ok = got(mb_v, i) && got(mb_p, i);
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t v_tile = sbase + Ly::V_OFF + (i & 1) * Ly::TILE;
@@ -412,7 +413,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   } else {
     // =============================================================== softmax
     for (int i = 0; i < nt; ++i) {
-      if (!__all_sync(~0u, got(mb_s, i)) || *fail) { *fail = 1; break; }
+      if (!__all_sync(~0u, got(mb_s, i))) { *fail = 1; break; }
       tc::fence_after_sync();
       const uint32_t tm_s = tmem + lane_base + Ly::TM_S + (i & 1) * kKeys;
       const float4* prm = reinterpret_cast<const float4*>(sm + Ly::UNIT_OFF + (i & 1) * kUnits * 16);
@@ -426,23 +427,28 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
         for (int x = 0; x < kKeys; ++x)
           if (x >= nvis) s[x / 32][x % 32] = 0xff800000u;
       }
-      float top[kUnits];  // largest score of each unit
+      constexpr int NU = ONE ? 1 : kUnits, UK = kKeys / NU;  // groups of keys under one pair of scales
+      float top[NU];  // largest score of each
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        float t = __uint_as_float(s[u / 2][16 * (u & 1)]);
+      for (int u = 0; u < NU; ++u) {
+        float t[4];
 #pragma unroll
-        for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[u / 2][16 * (u & 1) + x]));
-        top[u] = t;
+        for (int x = 0; x < 4; ++x) t[x] = __uint_as_float(s[(u * UK + x) / 32][(u * UK + x) % 32]);
+#pragma unroll
+        for (int x = 4; x < UK; ++x) t[x & 3] = fmaxf(t[x & 3], __uint_as_float(s[(u * UK + x) / 32][(u * UK + x) % 32]));
+        top[u] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
       }
       // the units' scales come with the V tile
       if (!__all_sync(~0u, got(mb_v, i))) { *fail = 1; break; }
-      float mx = -CUDART_INF_F;
+      float mx = -CUDART_INF_F, f1[NU], b1[NU], inv[NU], rest[NU];
       bool odd = false;  // a V scale below 2^-100
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
+      for (int u = 0; u < NU; ++u) {
         const float4 pr = prm[u];
         // at least 2^-120, so that -infinity stays itself; smaller factors meet scores that they make zero anyway
-        mx = fmaxf(mx, fmaf(top[u], fmaxf(fac * pr.x, 7.5231639e-37f), pr.y));
+        f1[u] = fmaxf(fac * pr.x, 7.5231639e-37f);
+        b1[u] = pr.y, rest[u] = pr.z, inv[u] = pr.w;
+        mx = fmaxf(mx, fmaf(top[u], f1[u], pr.y));
         odd |= pr.z != 1.f;
       }
       const bool up = mx > m + kSlack;  // m = -infinity: any
@@ -466,29 +472,27 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       }
       const float off = kOffset - (m == -CUDART_INF_F ? 0.f : m);
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        const float4 pr = prm[u];
-        const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f), b1 = pr.y + off;
-        const uint64_t f = pair(f1, f1), b = pair(b1, b1);
-        uint64_t sum = 0;  // two zeros
+      for (int u = 0; u < NU; ++u) {
+        const uint64_t f = pair(f1[u], f1[u]), b = pair(b1[u] + off, b1[u] + off);
+        uint64_t sum[2] = {0, 0};  // two zeros each
 #pragma unroll
-        for (int x = 0; x < 16; x += 2) {
+        for (int x = 0; x < UK; x += 2) {
+          const int k = u * UK + x;
           float e0, e1;
-          const uint32_t* z = &s[u / 2][16 * (u & 1) + x];
-          unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), f, b), e0, e1);
+          unpair(fma2(pair(__uint_as_float(s[k / 32][k % 32]), __uint_as_float(s[k / 32][k % 32 + 1])), f, b), e0, e1);
           e0 = fast_exp2(e0), e1 = fast_exp2(e1);
-          sum = add2(sum, pair(e0, e1));
-          s[0][8 * u + x / 2] = pack_f16(e0, e1);
+          sum[x / 2 & 1] = add2(sum[x / 2 & 1], pair(e0, e1));
+          s[0][k / 2] = pack_f16(e0, e1);
         }
         float s0, s1;
-        unpair(sum, s0, s1);
-        l = fmaf(s0 + s1, pr.w, l);
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l = fmaf(s0 + s1, inv[u], l);
         if (odd) {
-          const __half2 z = __float2half2_rn(pr.z);
+          const __half2 z = __float2half2_rn(rest[u]);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][8 * u + x]), z);
-            s[0][8 * u + x] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int x = 0; x < UK / 2; ++x) {
+            __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][u * UK / 2 + x]), z);
+            s[0][u * UK / 2 + x] = *reinterpret_cast<const uint32_t*>(&y);
           }
         }
       }
@@ -564,16 +568,24 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   }
 }
 
+template <int D, int KIND, bool ONE>
+cudaError_t launch_one(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks, int nsplit,
+                       bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
+  constexpr int smem = Layout<D>::BYTES;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_rows_kernel<D, KIND, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attn_rows_kernel<D, KIND, ONE><<<dim3(tiles, c.h_kv, nsplit), kThreads, smem, st>>>(c, p, q, h_q, split_blocks, nsplit,
+                                                                                      out, lse, part, status);
+  return cudaGetLastError();
+}
+
 template <int D, int KIND>
 cudaError_t launch(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks, int nsplit,
                    bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
-  constexpr int smem = Layout<D>::BYTES;
-  const cudaError_t e =
-      cudaFuncSetAttribute(attn_rows_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  attn_rows_kernel<D, KIND><<<dim3(tiles, c.h_kv, nsplit), kThreads, smem, st>>>(c, p, q, h_q, split_blocks, nsplit, out,
-                                                                               lse, part, status);
-  return cudaGetLastError();
+  return c.B >= kKeys
+             ? launch_one<D, KIND, true>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
+             : launch_one<D, KIND, false>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
 }
 
 }  // namespace
