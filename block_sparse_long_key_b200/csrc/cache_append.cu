@@ -34,6 +34,7 @@ namespace cache {
 namespace {
 
 constexpr int kFewTokens = 4;  // see append_kernel
+constexpr int kDoubts = 512;   // roundings in doubt held per tile
 
 struct RowInfo {
   int row, t_begin;  // the row's first new token
@@ -86,40 +87,49 @@ __device__ __forceinline__ float element(const uint4& u, int e) {
   return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
 }
 
-// k' of 8 channels of token rel.
-template <int D>
-__device__ __forceinline__ uint4 conv8(const View& c, const RowInfo& R, const bf16* k, const float* w, int head, int ch,
-                                       int rel) {
-  const int W = c.conv_width;
+// k' of 8 channels of a token; tap(l): their raw keys l tokens before.  w: the head's weights [d, W]; ws: the same as [W, d] in shared memory, or null (a
+// lane's 8 x W weights are then read one by one, which a CTA that converts many tokens would feel).
+// `doubt(e)` takes note of a channel whose rounding 32 bits do not settle and returns true, or returns false: then it is
+// settled here.
+template <int D, typename G, typename F>
+__device__ __forceinline__ uint4 conv8(int W, const float* w, const float* ws, int ch, G tap, F doubt) {
   uint4 raw[kMaxWidth];
 #pragma unroll
-  for (int l = 0; l < kMaxWidth; ++l) raw[l] = l < W ? raw_key<D>(c, R, k, head, ch, rel - l) : make_uint4(0, 0, 0, 0);
+  for (int l = 0; l < kMaxWidth; ++l) raw[l] = l < W ? tap(l) : make_uint4(0, 0, 0, 0);
   float x0[8], z[8], size[8];
   bf16x8_to_f32(raw[0], x0);
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = size[e] = 0.f;
-  const float* wc = w + ((size_t)head * D + ch) * W;
+  const float* wc = w + (size_t)ch * W;
 #pragma unroll
   for (int l = 0; l < kMaxWidth; ++l)
     if (l < W) {
-      float x[8];
+      float x[8], wl[8];
       bf16x8_to_f32(raw[l], x);
+      if (ws) {
+        *reinterpret_cast<float4*>(wl) = *reinterpret_cast<const float4*>(ws + l * D + ch);
+        *reinterpret_cast<float4*>(wl + 4) = *reinterpret_cast<const float4*>(ws + l * D + ch + 4);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wl[e] = __ldg(wc + e * W + l);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float wl = __ldg(wc + e * W + l);
-        z[e] = fmaf(wl, x[e], z[e]);
-        size[e] += fabsf(wl * x[e]);
+        z[e] = fmaf(wl[e], x[e], z[e]);
+        size[e] = fmaf(fabsf(wl[e]), fabsf(x[e]), size[e]);
       }
     }
   float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     y[e] = x0[e] + __fdividef(z[e], 1.f + __expf(-z[e]));
-    // sum: W 2^-24 size; SiLU: slope at most 1.1, its own error 2^-21 |z| (1 + |z| / 2^2 for the exponent's argument)
-    const float E = 9.5367432e-7f * (fabsf(x0[e]) + size[e] * (1.2f + 0.25f * fminf(fabsf(z[e]), 88.f)));
+    // In units of 2^-24: the sum is off by W size, SiLU (slope at most 1.1) carries that and adds 12 of its own value
+    // (exponential, quotient) and 2 |z| of its value for the exponent's argument (|z SiLU(z)| <= size where that
+    // counts), the last sum and the rounding to 32 bits 2 of the result.  1.1 W + 16 with room:
+    const float E = 5.9604645e-8f * (2.f * fabsf(x0[e]) + size[e] * (1.2f * (float)W + 18.f));
     const uint16_t a = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] - E));
     const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] + E));
-    if (a != b || !(fabsf(z[e]) < 80.f))
+    if ((a != b || !(fabsf(z[e]) < 80.f)) && !doubt(e))
       y[e] = conv_in_64(element(raw[0], e), element(raw[1], e), element(raw[2], e), element(raw[3], e), element(raw[4], e),
                         element(raw[5], e), element(raw[6], e), element(raw[7], e), wc + e * W, W);
   }
@@ -170,7 +180,8 @@ struct Shape {
   static constexpr int LANES = D / 8;               // threads across a token
   static constexpr int GROUPS = THREADS / LANES;    // token groups of NCH consecutive tokens
   static constexpr int STAGE = 2 * NCH * THREADS;   // 16-byte slots of one head's K and V
-  static constexpr int BYTES = 2 * STAGE * 16 + THREADS * 8 * 4;
+  static constexpr int RAW = (BLK + kMaxWidth - 1) * LANES;  // slots of a head's raw keys, with the taps before the block
+  static constexpr int bytes(bool conv) { return 2 * STAGE * 16 + THREADS * 8 * 4 + (conv ? 2 * RAW * 16 : 0); }
   static_assert(NCH * GROUPS == BLK, "tile");
 };
 
@@ -230,7 +241,10 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
   extern __shared__ __align__(16) unsigned char smem[];
   uint4* ring = reinterpret_cast<uint4*>(smem);                            // [2][K, V][NCH][THREADS]
   float* gsum = reinterpret_cast<float*>(smem + 2 * S::STAGE * 16);        // [GROUPS][D], swizzled
+  uint4* raws = reinterpret_cast<uint4*>(smem + 2 * S::STAGE * 16 + THREADS * 8 * 4);  // [2][BLK + 7][LANES], conv only
   __shared__ float red[2][THREADS / 32];
+  __shared__ int n_doubt, doubts[CONV ? kDoubts : 1];
+  __shared__ __align__(16) float wsm[CONV ? 2 * kMaxWidth * D : 4];  // two heads' conv weights [W, d]
   const int tid = threadIdx.x, u = blockIdx.x;
   const int head0 = blockIdx.y * heads_per_cta, head1 = min(c.h_kv, head0 + heads_per_cta);
   const int ch = tid % LANES * 8, off0 = tid / LANES * NCH;  // this thread's channels and first token of a block
@@ -287,6 +301,13 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
   const bool has_old = R.pos0 % B != 0;
   bool bad = false;
 
+  // k' straight from memory
+  auto key_now = [&](int head, int rel) {
+    if constexpr (CONV)
+      return conv8<D>(c.conv_width, w + (size_t)head * D * c.conv_width, nullptr, ch,
+                      [&](int l) { return raw_key<D>(c, R, k, head, ch, rel - l); }, [](int) { return false; });
+    else return raw_key<D>(c, R, k, head, ch, rel);
+  };
   if (R.n <= kFewTokens && R.n == n_first && R.len % B != 0) {
     // A few tokens of an unfinished block (a generated token, mostly): one CTA for all heads, a thread group per
     // (token, head).  With a CTA per head, one group in 16 would work.
@@ -295,9 +316,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
       const int rel = i / c.h_kv, head = i % c.h_kv;
       const size_t at = ((size_t)(R.t_begin + rel) * c.h_kv + head) * D + ch;
       const uint4 y = __ldg(reinterpret_cast<const uint4*>(v + at));
-      uint4 x;
-      if constexpr (CONV) x = conv8<D>(c, R, k, w, head, ch, rel);
-      else x = raw_key<D>(c, R, k, head, ch, rel);
+      const uint4 x = key_now(head, rel);
       *tail_at<D>(c.tail_k, c, R.row, j0, head, R.pos0 % B + rel, ch) = finite8(x, &bad);
       *tail_at<D>(c.tail_v, c, R.row, j0, head, R.pos0 % B + rel, ch) = finite8(y, &bad);
     }
@@ -340,18 +359,76 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
           if (!CONV || !fresh) cp_async16_zfill(dst + i * THREADS, ks, old || fresh);
           cp_async16_zfill(dst + (NCH + i) * THREADS, vs, old || fresh);
         }
+        if constexpr (CONV) {  // raw keys of the new tokens and of the W - 1 before them
+          uint4* rd = raws + ((head - head0) & 1) * S::RAW;
+          for (int i = tid; i < S::RAW; i += THREADS) {
+            const int off = i / LANES - (kMaxWidth - 1), rel = rel0 + off, cc = i % LANES * 8;
+            if (off < lo - Wm1 || off >= hi) continue;
+            const bf16* at = k;
+            if (rel >= 0) at = k + ((size_t)(R.t_begin + rel) * c.h_kv + head) * D + cc;
+            else if (R.pos0 + rel >= 0)
+              at = c.hist + (((size_t)R.row * kHistRing + ((R.pos0 + rel) & (kHistRing - 1))) * c.h_kv + head) * D + cc;
+            cp_async16_zfill(rd + i, at, R.pos0 + rel >= 0);
+          }
+        }
       }
       cp_async_commit();
     };
     fetch(head0);
+    // the next head's conv weights wait in registers; [d, W] goes to [W, d]
+    constexpr int NWR = CONV ? kMaxWidth * D / THREADS : 1;
+    float wnext[NWR];
+    auto ask_weights = [&](int head) {
+      if constexpr (CONV) {
+#pragma unroll
+        for (int i = 0; i < NWR; ++i)
+          if (tid + i * THREADS < D * c.conv_width && head < head1)
+            wnext[i] = __ldg(w + (size_t)head * D * c.conv_width + tid + i * THREADS);
+      }
+    };
+    ask_weights(head0);
     for (int head = head0; head < head1; ++head) {
       fetch(head + 1);
       uint4 x[NCH], y[NCH];
       uint4* src = ring + ((head - head0) & 1) * S::STAGE + tid;
       if constexpr (CONV) {  // the converted tokens go where copies of the others go
+        const uint4* rs = raws + ((head - head0) & 1) * S::RAW + (kMaxWidth - 1) * LANES;
+        float* ws = wsm + (head & 1) * kMaxWidth * D;
+        const float* wh = w + (size_t)head * D * c.conv_width;
+        const int W = c.conv_width;
+#pragma unroll
+        for (int i = 0; i < NWR; ++i)
+          if (tid + i * THREADS < D * W) ws[(tid + i * THREADS) % W * D + (tid + i * THREADS) / W] = wnext[i];
+        ask_weights(head + 1);
+        if (tid == 0) n_doubt = 0;
+        cp_async_wait<1>();
+        __syncthreads();
+        // Roundings in doubt are noted and settled together, a thread each.
         const int i1 = min(hi - off0, NCH);
 #pragma unroll 1
-        for (int i = max(lo - off0, 0); i < i1; ++i) src[i * THREADS] = conv8<D>(c, R, k, w, head, ch, rel0 + off0 + i);
+        for (int i = max(lo - off0, 0); i < i1; ++i)
+          src[i * THREADS] = conv8<D>(W, wh, ws, ch, [&](int l) { return rs[(off0 + i - l) * LANES + ch / 8]; },
+                                      [&](int e) {
+                                        const int at = atomicAdd(&n_doubt, 1);
+                                        if (at >= kDoubts) return false;
+                                        doubts[at] = (off0 + i) * D + ch + e;
+                                        return true;
+                                      });
+        __syncthreads();
+        if (n_doubt > 0) {
+          for (int at = tid; at < min(n_doubt, kDoubts); at += THREADS) {
+            const int off = doubts[at] / D, cc = doubts[at] % D;
+            float xs[kMaxWidth];
+#pragma unroll
+            for (int l = 0; l < kMaxWidth; ++l)
+              xs[l] = l < W ? __bfloat162float(reinterpret_cast<const bf16*>(rs + (off - l) * LANES)[cc]) : 0.f;
+            const float z = conv_in_64(xs[0], xs[1], xs[2], xs[3], xs[4], xs[5], xs[6], xs[7], wh + (size_t)cc * W, W);
+            // into the slot of the thread that holds it
+            uint4* slot = ring + ((head - head0) & 1) * S::STAGE + off % NCH * THREADS + off / NCH * LANES + cc / 8;
+            reinterpret_cast<bf16*>(slot)[cc & 7] = __float2bfloat16_rn(z);
+          }
+          __syncthreads();
+        }
       }
       cp_async_wait<1>();
 #pragma unroll
@@ -414,9 +491,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
       if (replace) {
         const int hi = min(R.len - jc * B, B), rel0 = jc * B - R.pos0;
         for (int off = off0; off < min(off0 + NCH, hi); ++off) {
-          uint4 x;
-          if constexpr (CONV) x = conv8<D>(c, R, k, w, head, ch, rel0 + off);
-          else x = raw_key<D>(c, R, k, head, ch, rel0 + off);
+          const uint4 x = key_now(head, rel0 + off);
           const size_t at = ((size_t)(R.t_begin + rel0 + off) * c.h_kv + head) * D + ch;
           *tail_at<D>(c.tail_k, c, R.row, jc, head, off, ch) = finite8(x, &bad);
           *tail_at<D>(c.tail_v, c, R.row, jc, head, off, ch) = finite8(__ldg(reinterpret_cast<const uint4*>(v + at)), &bad);
@@ -452,14 +527,14 @@ cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* 
   cudaError_t e;
   if (c.conv_width > 0) {
     if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  S::BYTES)) != cudaSuccess)
+                                  S::bytes(true))) != cudaSuccess)
       return e;
-    append_kernel<KIND, D, BLK, true><<<grid, S::THREADS, S::BYTES, st>>>(c, p, k, v, w, per_token, (int)per, status);
+    append_kernel<KIND, D, BLK, true><<<grid, S::THREADS, S::bytes(true), st>>>(c, p, k, v, w, per_token, (int)per, status);
   } else {
     if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  S::BYTES)) != cudaSuccess)
+                                  S::bytes(false))) != cudaSuccess)
       return e;
-    append_kernel<KIND, D, BLK, false><<<grid, S::THREADS, S::BYTES, st>>>(c, p, k, v, w, per_token, (int)per, status);
+    append_kernel<KIND, D, BLK, false><<<grid, S::THREADS, S::bytes(false), st>>>(c, p, k, v, w, per_token, (int)per, status);
   }
   return cudaGetLastError();
 }

@@ -682,37 +682,73 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   }
 }
 
-// Joins the splits of one (token, query head) per warp.
-template <int D>
+// Joins the splits of a (token, query head): WARPS warps take its splits in turn, four at a time in flight.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128)
 merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float* __restrict__ part,
              bf16* __restrict__ out, float* __restrict__ lse) {
   constexpr int kORow = Layout<D>::kORow, E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const size_t item = (size_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  __shared__ float so[WARPS > 1 ? 4 : 1][D], sm[4], sl[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t item = (size_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
   if (item >= (size_t)p.T * h_q) return;
-  const int tok = (int)(item / h_q), row = __ldg(p.row + tok);
+  const int tok = (int)(item / h_q), row = __ldg(p.row + tok), pos = __ldg(p.pos + tok);
   if ((unsigned)row >= (unsigned)c.rows) return;
-  const int pos = __ldg(p.pos + tok);
+  const int lb = 31 - __clz(c.B);
   // splits that wrote: as many as the tile's furthest row needs; a row's own are the first of those
-  const int n = pos < 0 || pos >= c.state[2 * row] || pos / c.B >= c.state[2 * row + 1] ? 0 : pos / c.B / split_blocks + 1;
+  const int n = pos < 0 || pos >= c.state[2 * row] || pos >> lb >= c.state[2 * row + 1] ? 0 : (pos >> lb) / split_blocks + 1;
   const float* b = part + item * nsplit * kORow;
   float M = -CUDART_INF_F, l = 0.f, o[E];
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, b[s * kORow + D]);
-  for (int s = 0; s < n; ++s) {
-    const float m = b[s * kORow + D], ls = b[s * kORow + D + 1];
-    const float a = m == -CUDART_INF_F ? (ls == ls ? 0.f : 1.f) : fast_exp2(m - M);
-    l += a * ls;
+  for (int s0 = warp % WARPS * 4; s0 < n; s0 += 4 * WARPS) {
+    float m[4], ls[4], v[4][E], top = M;
 #pragma unroll
-    for (int x = 0; x < E; ++x) o[x] += a * b[s * kORow + lane * E + x];
+    for (int i = 0; i < 4; ++i) {
+      const float* d = b + min(s0 + i, n - 1) * kORow;
+      m[i] = s0 + i < n ? d[D] : -CUDART_INF_F;
+      ls[i] = s0 + i < n ? d[D + 1] : 0.f;
+#pragma unroll
+      for (int x = 0; x < E; ++x) v[i][x] = d[lane + 32 * x];
+      top = fmaxf(top, m[i]);
+    }
+    const float a0 = M == -CUDART_INF_F ? 0.f : fast_exp2(M - top);
+    l *= a0;
+#pragma unroll
+    for (int x = 0; x < E; ++x) o[x] *= a0;
+    M = top;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = m[i] == -CUDART_INF_F ? (ls[i] == ls[i] ? 0.f : 1.f) : fast_exp2(m[i] - top);
+      l += a * ls[i];
+#pragma unroll
+      for (int x = 0; x < E; ++x) o[x] += s0 + i < n ? a * v[i][x] : 0.f;
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / (32768.f * l);
+  if constexpr (WARPS == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / (32768.f * l);
 #pragma unroll
-  for (int x = 0; x < E; x += 2)
-    *reinterpret_cast<uint32_t*>(out + item * D + lane * E + x) = pack_bf16(o[x] * inv, o[x + 1] * inv);
-  if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
+    for (int x = 0; x < E; ++x) out[item * D + lane + 32 * x] = __float2bfloat16_rn(l == 0.f ? 0.f : o[x] * inv);
+    if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
+  } else {
+#pragma unroll
+  for (int x = 0; x < E; ++x) so[warp][lane + 32 * x] = o[x];
+  if (lane == 0) sm[warp] = M, sl[warp] = l;
+  __syncthreads();
+  const int ch = threadIdx.x;
+  if (ch >= D) return;
+  M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+  l = 0.f;
+  float y = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float a = sm[w] == -CUDART_INF_F ? (sl[w] == sl[w] ? 0.f : 1.f) : fast_exp2(sm[w] - M);
+    l += a * sl[w];
+    y += a * so[w][ch];
+  }
+  out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (32768.f * l));
+  if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
+  }
 }
 
 // How a step over all blocks is cut up.
@@ -736,7 +772,9 @@ Cut cut_of(const View& c, int T, int h_q) {
   x.per_token = a <= b;
   x.wide = !x.per_token || G > 8;
   x.tiles = x.per_token ? a : b;
-  x.many = x.tiles >= 2 * big;
+  // A tile of 128 rows takes about as long as three of 16 (16 rows of 64 and of 32 query rows each over 13K keys:
+  // 338 and 330 us in tiles of 128, 500 and 250 in tiles of 16).
+  x.many = x.tiles >= 3 * big;
   if (x.many) x.tiles = (long long)T * G / 128 + c.rows;
   const long long ctas = (x.many ? big : x.tiles) * c.h_kv;
   const long long want = ((x.many ? 4 : 16) * 148 + ctas - 1) / ctas;
@@ -786,7 +824,11 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
                                          part, status, st);
   if (e != cudaSuccess || x.nsplit == 1) return e;
   const long long items = (long long)p.T * h_q;
-  merge_kernel<D><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
+  // (measured with 38K rows of 2 splits: a warp each 438 us in all, a CTA each 472; 32 rows of 64: 61 and 44)
+  if (x.nsplit <= 8)
+    merge_kernel<D, 1><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
+  else
+    merge_kernel<D, 4><<<(unsigned)items, 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
   return cudaGetLastError();
 }
 
