@@ -119,21 +119,33 @@ __device__ __forceinline__ uint4 conv8(int W, const float* w, const float* ws, i
         size[e] = fmaf(fabsf(wl[e]), fabsf(x[e]), size[e]);
       }
     }
+  // In units of 2^-24: the sum is off by W size, SiLU (slope at most 1.1) carries that and adds 12 of its own value
+  // (exponential, quotient) and 2 |z| of its value for the exponent's argument (|z SiLU(z)| <= size where that counts),
+  // the last sum and the rounding to 32 bits 2 of the result.  1.1 W + 16 with room:
+  const float e1 = 5.9604645e-8f * (1.2f * (float)W + 18.f);
   float y[8];
+  uint32_t open = 0;  // channels whose rounding is not settled
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     y[e] = x0[e] + __fdividef(z[e], 1.f + __expf(-z[e]));
-    // In units of 2^-24: the sum is off by W size, SiLU (slope at most 1.1) carries that and adds 12 of its own value
-    // (exponential, quotient) and 2 |z| of its value for the exponent's argument (|z SiLU(z)| <= size where that
-    // counts), the last sum and the rounding to 32 bits 2 of the result.  1.1 W + 16 with room:
-    const float E = 5.9604645e-8f * (2.f * fabsf(x0[e]) + size[e] * (1.2f * (float)W + 18.f));
-    const uint16_t a = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] - E));
-    const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(y[e] + E));
-    if ((a != b || !(fabsf(z[e]) < 80.f)) && !doubt(e))
-      y[e] = conv_in_64(element(raw[0], e), element(raw[1], e), element(raw[2], e), element(raw[3], e), element(raw[4], e),
-                        element(raw[5], e), element(raw[6], e), element(raw[7], e), wc + e * W, W);
+    const float E = fmaf(size[e], e1, 1.1920929e-7f * fabsf(x0[e]));
+    const uint32_t both = pack_bf16(y[e] - E, y[e] + E);
+    open |= (uint32_t)(__byte_perm(both, 0, 0x1032) != both || !(fabsf(z[e]) < 80.f)) << e;
   }
-  return f32_to_bf16x8(y);
+  uint4 r = f32_to_bf16x8(y);
+  while (open) {
+    const int e = __ffs(open) - 1;
+    open &= open - 1;
+    if (doubt(e)) continue;
+    const float v = conv_in_64(element(raw[0], e), element(raw[1], e), element(raw[2], e), element(raw[3], e),
+                               element(raw[4], e), element(raw[5], e), element(raw[6], e), element(raw[7], e), wc + e * W, W);
+    const uint32_t h = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    uint32_t* word = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e >> 1 == i) word[i] = e & 1 ? (word[i] & 0xffffu) | h << 16 : (word[i] & 0xffff0000u) | h;
+  }
+  return r;
 }
 
 template <int D>
@@ -378,11 +390,17 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     // the next head's conv weights wait in registers; [d, W] goes to [W, d]
     constexpr int NWR = CONV ? kMaxWidth * D / THREADS : 1;
     float wnext[NWR];
+    int wplace[NWR];
+#pragma unroll
+    for (int i = 0; i < NWR; ++i) {
+      const int at = tid + i * THREADS, W = CONV ? c.conv_width : 1;
+      wplace[i] = at < D * W ? at % W * D + at / W : -1;
+    }
     auto ask_weights = [&](int head) {
       if constexpr (CONV) {
 #pragma unroll
         for (int i = 0; i < NWR; ++i)
-          if (tid + i * THREADS < D * c.conv_width && head < head1)
+          if (wplace[i] >= 0 && head < head1)
             wnext[i] = __ldg(w + (size_t)head * D * c.conv_width + tid + i * THREADS);
       }
     };
@@ -398,7 +416,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         const int W = c.conv_width;
 #pragma unroll
         for (int i = 0; i < NWR; ++i)
-          if (tid + i * THREADS < D * W) ws[(tid + i * THREADS) % W * D + (tid + i * THREADS) / W] = wnext[i];
+          if (wplace[i] >= 0) ws[wplace[i]] = wnext[i];
         ask_weights(head + 1);
         if (tid == 0) n_doubt = 0;
         cp_async_wait<1>();
