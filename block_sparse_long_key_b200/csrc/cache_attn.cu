@@ -17,7 +17,7 @@
 // from the unrounded ones.
 //
 // A partial block is bf16 (the tail) and is multiplied as bf16, its weights
-// as hi + lo.
+// 2^(s_i log2 e - M + 15) as hi + lo; in M it counts with its largest |v| / 448.
 //
 // Fragments (mma.m16n8k16; lane = 4 g + t).  Keys come 16 tokens (a unit) at a
 // time and are the M side of both products, so that up to 8 query rows (the
@@ -294,6 +294,24 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
       }
     }
   }
+  // The reference takes the unit's V at its largest magnitude, as it takes a page at its scale.
+  uint4 w[D / 64][4];
+  float am = 0.f;
+#pragma unroll
+  for (int half = 0; half < D / 64; ++half)  // 8 channels per lane at a time
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[half][i] = make_uint4(0, 0, 0, 0);
+      if (first + 4 * t + i < n_tok)
+        w[half][i] = *reinterpret_cast<const uint4*>(tv + (size_t)(first + 4 * t + i) * D + (D / 8) * g + 8 * half);
+      float f[8];
+      bf16x8_to_f32(w[half][i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(f[e]));
+    }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) am = fmaxf(am, __shfl_xor_sync(~0u, am, off));
+  const float lv = log2f(fmaxf(am * (1.f / 448.f), 7.8886090522101181e-31f));
   const float fac = kLog2e * rsqrtf((float)D);
   float mx[NT][2];
 #pragma unroll
@@ -303,10 +321,11 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
     for (int x = 0; x < 4; ++x) {
       const int tok = r + (x & 2), b = x & 1;
       s[n][x] = tok < n_tok && pos_first + tok <= pos[n][b] ? s[n][x] * fac : -CUDART_INF_F;
-      mx[n][b] = fmaxf(mx[n][b], s[n][x]);
+      mx[n][b] = fmaxf(mx[n][b], s[n][x] + lv);
     }
   }
   st.raise(mx);
+  // weights 2^(s - M + 15): at most 2^(15 - lv), within bf16
   uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -325,15 +344,8 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
     }
   }
 #pragma unroll
-  for (int half = 0; half < D / 64; ++half) {  // 8 channels per lane at a time
-    uint4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (first + 4 * t + i < n_tok)
-        w[i] = *reinterpret_cast<const uint4*>(tv + (size_t)(first + 4 * t + i) * D + (D / 8) * g + 8 * half);
-    }
-    const uint32_t* ww[4] = {&w[0].x, &w[1].x, &w[2].x, &w[3].x};
+  for (int half = 0; half < D / 64; ++half) {
+    const uint32_t* ww[4] = {&w[half][0].x, &w[half][1].x, &w[half][2].x, &w[half][3].x};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t a[4] = {__byte_perm(ww[0][i], ww[1][i], 0x5410), __byte_perm(ww[0][i], ww[1][i], 0x7632),

@@ -118,7 +118,7 @@ class Run:
         for x in (self.c.k_scale, self.c.v_scale, self.c.cent, self.c.tail_k, self.c.tail_v):
             x.fill_(float("nan"))
         self.ref = cr.RefCache(rows, n_pages, max_blocks, h_kv, d, B, kind, W)
-        self.hq, self.topk, self.scale = h_q, topk, scale
+        self.hq, self.topk, self.scale, self.check = h_q, topk, scale, True
         self.gen = torch.Generator().manual_seed(seed)
         self.w = torch.rand((h_kv, d, W), generator=self.gen) - 0.5 if W else None
 
@@ -156,6 +156,8 @@ class Run:
                           workspace=ws)
         status = moba.check_status(ws)
         r.append(want[0], want[4], k, v, self.w)
+        if self.check:
+            self.check_store()
         return status
 
     def check_store(self, rows=None):
@@ -216,7 +218,6 @@ class Run:
         assert st == 0
         if plan.token_row.shape[0]:
             assert self.append(plan, want) == 0
-            self.check_store()
             self.queries(plan, want, dense=dense)
 
 
@@ -352,3 +353,434 @@ def test_routing_in_slabs():
     x = torch.einsum("thd,jd->thj", q.double(), held[:39, 0])
     want = torch.sort(x, dim=-1, descending=True, stable=True).indices[..., :5].sort(-1).values
     assert torch.equal(sel[..., :5].long(), want) and (sel[..., 5] == 39).all()
+
+
+# --------------------------------------------------------------------------------------------------------- bookkeeping
+def _tables_only(rows, n_pages, max_blocks, B):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    return moba.Cache(rows=rows, n_pages=n_pages, max_blocks=max_blocks, h_kv=1, head_dim=64, block_size=B,
+                      block_table=torch.full((rows, max_blocks), -1, **i32), row_state=torch.zeros((rows, 2), **i32),
+                      free_pages=torch.arange(n_pages, **i32), ring=torch.tensor([0, n_pages], device="cuda"))
+
+
+def _check_tables(c, ref, new_len, T, **kw):
+    ws = c.alloc_workspace(0)
+    plan = moba.cache_tables(c, torch.tensor(new_len, dtype=torch.int32, device="cuda"), T, workspace=ws, **kw)
+    status = moba.check_status(ws)
+    want = ref.tables(new_len, T)
+    for got, exp, name in zip(plan, want, ("cu", "row", "pos", "slot")):
+        assert got.tolist() == exp, name
+    return status, want
+
+
+@gpu
+@pytest.mark.parametrize("rows,scale", [(7, 40), (1500, 12), (300, 300)])
+def test_tables_over_many_steps(rows, scale):
+    """Pages wander through the ring: growth, release, refusals, rows of nothing; one CTA's worth of rows and more, steps
+    that end in the first launch and that need the second."""
+    B, g = 16, torch.Generator().manual_seed(rows)
+    n_pages = rows * scale // B // 2 + 9
+    c, ref = _tables_only(rows, n_pages, 3 * scale // B + 4, B), cr.RefCache(rows, n_pages, 3 * scale // B + 4, 1, 64, B, "e4m3", 0)
+    seen = 0
+    for step in range(12):
+        new = torch.randint(0, scale, (rows,), generator=g)
+        new[torch.rand(rows, generator=g) < 0.3] = 0
+        new[torch.rand(rows, generator=g) < 0.2] = -1
+        new = new.tolist()
+        T = sum(max(n, 0) for n in new) + (step % 3)
+        status, want = _check_tables(c, ref, new, T)
+        assert bool(status & moba.STATUS_NO_PAGES) == bool(want[4])
+        assert status & ~moba.STATUS_NO_PAGES == 0
+        seen |= bool(want[4])
+        head, tail = c.ring.tolist()
+        ring = c.free_pages.tolist()
+        assert [ring[i % n_pages] for i in range(head, tail)] == list(ref.free)
+        assert c.row_state.tolist() == [[a, len(b)] for a, b in zip(ref.length, ref.pages)]
+    assert seen and head > n_pages        # refusals happened, and the ring went round
+
+
+@gpu
+def test_tables_refuse_more_tokens_and_blocks_than_there_is_room_for():
+    c, ref = _tables_only(4, 100, 3, 16), cr.RefCache(4, 100, 3, 1, 64, 16, "e4m3", 0)
+    status, want = _check_tables(c, ref, [48, 49, 5, 5], 107)
+    assert status == moba.STATUS_NO_PAGES and want[4] == [1]
+    status, want = _check_tables(c, ref, [0, 3, 40, 9], 40)          # row 2 runs past the token arrays, row 3 begins there
+    assert status == moba.STATUS_BAD_SEQLENS and want[4] == [2, 3]
+    assert _check_tables(c, ref, [0, 0, 0, 0], 0)[0] == 0            # nothing at all
+    assert _check_tables(c, ref, [-1, -1, -1, -1], 3)[0] == 0
+    assert c.row_state.tolist() == [[0, 0]] * 4
+
+
+@gpu
+def test_tables_out_of_place_plan_the_same_step_again():
+    B = 32
+    c, ref = _tables_only(5, 40, 9, B), cr.RefCache(5, 40, 9, 1, 64, B, "e4m3", 0)
+    _check_tables(c, ref, [70, 3, 0, 31, 33], 137)
+    state, ring = c.row_state.clone(), c.ring.clone()
+    so, ro = torch.empty_like(state), torch.empty_like(ring)
+    new = [2, 40, 1, -1, 31]
+    ws = c.alloc_workspace(0)
+    first = None
+    for _ in range(3):
+        p = moba.cache_tables(c, torch.tensor(new, dtype=torch.int32, device="cuda"), 74, row_state_out=so, ring_out=ro, workspace=ws)
+        got = [x.tolist() for x in p] + [so.tolist(), ro.tolist()]
+        assert first is None or got == first
+        first = got
+        assert torch.equal(c.row_state, state) and torch.equal(c.ring, ring)
+    _check_tables(c, ref, new, 74)
+    assert torch.equal(c.row_state, so) and torch.equal(c.ring, ro)
+
+
+@gpu
+def test_tables_flag_states_that_cannot_be():
+    c = _tables_only(4, 20, 4, 16)
+    c.row_state[:] = torch.tensor([[-1, 0], [40, 2], [5, 9], [16, 1]], dtype=torch.int32)
+    c.block_table[3, 0] = 99                                        # a page that does not exist
+    ws = c.alloc_workspace(0)
+    p = moba.cache_tables(c, torch.tensor([1, 1, 1, 1], dtype=torch.int32, device="cuda"), 4, workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_BAD_TABLE
+    assert p.token_pos.tolist() == [-1, -1, -1, 16]
+    c.ring[:] = torch.tensor([5, 2])
+    moba.cache_tables(c, torch.tensor([0, 0, 0, 1], dtype=torch.int32, device="cuda"), 1, workspace=ws)
+    assert moba.check_status(ws) & moba.STATUS_BAD_TABLE
+
+
+# ----------------------------------------------------------------------------------------------------- hard conditions
+@gpu
+def test_refused_rows_are_not_written_and_see_nothing():
+    r = Run(3, 6, 8, 2, 1, 64, 16, "e4m3", 3, 2, seed=5)
+    plan, want, st = r.tables([40, 0, 10])
+    assert st == 0 and r.append(plan, want) == 0
+    plan, want, st = r.tables([3, 60, 3])                            # row 1 asks for more pages than are left
+    assert st == moba.STATUS_NO_PAGES and want[4] == [1]
+    before = r.c.tail_k[1].clone(), r.c.hist[1].clone(), r.c.k.view(torch.uint8).clone()
+    assert r.append(plan, want) == 0
+    r.check_store()
+    assert torch.equal(r.c.tail_k[1].view(torch.int16), before[0].view(torch.int16)) and torch.equal(r.c.hist[1], before[1])
+    sel = r.queries(plan, want)                                      # its rows: zeros, -infinity, -1
+    dead = [i for i, x in enumerate(want[1]) if x == 1]
+    assert (sel[dead] == -1).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_nan_and_infinite_tokens_are_stored_as_zero(kind):
+    r = Run(2, 20, 8, 2, 2, 64, 16, kind, 0, 3, seed=1)
+    plan, want, _ = r.tables([21, 3])
+    k, v = r.rand(24, 2, 64), r.rand(24, 2, 64)
+    for t, x in ((0, float("nan")), (5, float("inf")), (17, -float("inf")), (22, float("nan"))):
+        k[t, 0, 3], v[t, 1, 60] = x, x
+    ref_k = torch.where(torch.isfinite(k), k, 0)
+    ws = r.c.alloc_workspace(24, 2)
+    moba.cache_append(r.c, plan, k.cuda(), v.cuda(), workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_NONFINITE
+    r.ref.append(want[0], want[4], ref_k, torch.where(torch.isfinite(v), v, 0), None)
+    r.check_store()
+    r.queries(plan, want)
+
+
+@gpu
+@pytest.mark.parametrize("W", [0, 4])
+def test_a_length_set_back_and_written_again(W):
+    """Rejected drafts: lengths go back by up to a block (with the conv by at most 17 - W), across a block's end."""
+    B = 32
+    r = Run(2, 40, 12, 2, 1, 64, B, "e4m3", W, 3, seed=W)
+    r.step([B * 2 + 30, B - 2])
+    for back, again in ((5, 4), (12, 13), (13, 1), (1, 30)):
+        plan, want, st = r.tables([back, back])
+        assert r.append(plan, want) == 0
+        r.check_store()
+        for i in range(2):                                            # the drafts are rejected: their pages stay
+            r.ref.length[i] -= back
+        r.c.row_state[:, 0] -= back
+        r.step([again, again])
+
+
+@gpu
+@pytest.mark.parametrize("what", ["zero_v", "zero_k", "huge", "tiny", "spread", "denormal"])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 70])        # tiles of 8 and of 128 query rows
+def test_scales_of_every_size(what, kind, n):
+    r = Run(1, 40, 20, 4, 1, 64, 32, kind, 0, 4, seed=3)
+    T = 200
+    plan, want, _ = r.tables([T])
+    k, v = r.rand(T, 1, 64), r.rand(T, 1, 64)
+    blk = (torch.arange(T) // 32)[:, None, None]
+    if what == "zero_v":
+        v[:] = 0
+    elif what == "zero_k":
+        k[:] = 0
+    elif what == "huge":
+        v = (v.float() * 1e30).to(torch.bfloat16)
+    elif what == "tiny":
+        v, k = (v.float() * 1e-30).to(torch.bfloat16), (k.float() * 1e-30).to(torch.bfloat16)
+    elif what == "denormal":                                          # scales at their lower end
+        v = (v.float() * 1e-37).to(torch.bfloat16)
+    else:                                                             # blocks 2^12 apart from one another
+        v = (v.float() * torch.pow(2.0, 12.0 * (blk % 3 - 1))).to(torch.bfloat16)
+    assert r.append(plan, want, k, v) == 0
+    r.check_store()
+    plan, want, _ = r.tables([n])
+    assert r.append(plan, want, r.rand(n, 1, 64) * 0 if what in ("zero_v", "tiny", "denormal") else None,
+                    r.rand(n, 1, 64) * 0 if what in ("zero_v", "tiny", "denormal") else None) == 0
+    q = r.rand(n, 4, 64)
+    if what == "denormal":
+        # values near 1e-37: what a result loses to the smallest 32-bit numbers is not in the bound; it is small and finite
+        ws = r.c.alloc_workspace(n, 4)
+        out, lse = moba.cache_attention(r.c, plan, q.cuda(), workspace=ws)
+        o, l, mass, size, low = r.ref.attend(want[1], want[2], q)
+        assert (out.cpu().double() - o).abs().max() <= 1e-37 and (lse.cpu().double() - l).abs().max() <= 1e-4
+        return
+    r.queries(plan, want, q)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 90])
+def test_a_bad_query_spoils_its_own_row_only(n):
+    r = Run(1, 40, 20, 4, 1, 64, 32, "e4m3", 0, 4, seed=9)
+    plan, want, _ = r.tables([150])
+    r.append(plan, want)
+    plan, want, _ = r.tables([n])
+    r.append(plan, want)
+    q = r.rand(n, 4, 64)
+    ws = r.c.alloc_workspace(n, 4)
+    clean = [x.clone() for x in moba.cache_attention(r.c, plan, q.cuda(), workspace=ws)]
+    q[n - 1, 2, 7] = float("nan")
+    q[0, 1, 0] = float("inf")
+    for sel in (None, moba.cache_route(r.c, plan, q.cuda(), 64, workspace=ws)):
+        out, lse = moba.cache_attention(r.c, plan, q.cuda(), sel_idx=sel, workspace=ws)
+        bad = torch.zeros((n, 4), dtype=torch.bool)
+        bad[n - 1, 2] = bad[0, 1] = True
+        assert torch.isnan(out.cpu()[bad]).all() and torch.isnan(lse.cpu()[bad]).all()
+        assert torch.isfinite(out.cpu()[~bad].float()).all()
+        if sel is None:
+            assert torch.equal(out.cpu()[~bad], clean[0].cpu()[~bad]) and torch.equal(lse.cpu()[~bad], clean[1].cpu()[~bad])
+    assert moba.check_status(ws) == 0
+
+
+@gpu
+def test_selections_out_of_range_or_out_of_order_are_skipped():
+    r = Run(2, 40, 20, 2, 2, 64, 16, "int8", 0, 6, seed=2)
+    plan, want, _ = r.tables([100, 90])
+    r.append(plan, want)
+    plan, want, _ = r.tables([1, 1])
+    r.append(plan, want)
+    q = r.rand(2, 2, 64)
+    own = [100 // 16, 90 // 16]
+    sel = torch.tensor([[[0, 2, 2, 1, own[0], -1], [-1, -1, -1, -1, -1, -1]],
+                        [[3, own[1], 9, 1000000, -5, -1], [-1, 1, -1, 4, -1, own[1]]]], dtype=torch.int32)
+    seen = torch.tensor([[[0, 2, own[0]] + [-1] * 3, [-1] * 6], [[3, own[1]] + [-1] * 4, [1, 4, own[1]] + [-1] * 3]], dtype=torch.int32)
+    ws = r.c.alloc_workspace(2, 2)
+    out, lse = moba.cache_attention(r.c, plan, q.cuda(), sel_idx=sel.cuda(), workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_BAD_SEL_IDX
+    ref = r.ref.attend(want[1], want[2], q, seen)
+    cr.check_attention(out.cpu(), lse.cpu(), ref, 64)
+    assert (out[0, 1] == 0).all() and lse[0, 1] == -float("inf")
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 64])
+def test_pages_out_of_range_are_skipped(n):
+    r = Run(1, 40, 20, 2, 2, 64, 16, "e4m3", 0, 3, seed=4)
+    plan, want, _ = r.tables([100])
+    r.append(plan, want)
+    plan, want, _ = r.tables([n])
+    r.append(plan, want)
+    q = r.rand(n, 2, 64)
+    ws = r.c.alloc_workspace(n, 2)
+    good = r.c.block_table.clone()
+    r.c.block_table[0, 2], r.c.block_table[0, 4] = -3, 40
+    out, lse = moba.cache_attention(r.c, plan, q.cuda(), workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_BAD_TABLE
+    every = torch.tensor([[[j if j not in (2, 4) and j <= p // 16 else -1 for j in range(20)]] * 2 for p in want[2]], dtype=torch.int32)
+    cr.check_attention(out.cpu(), lse.cpu(), r.ref.attend(want[1], want[2], q, every), 64)
+    moba.cache_route(r.c, plan, q.cuda(), 3, workspace=ws)           # ends, whatever it picks
+    assert moba.check_status(ws) in (0, moba.STATUS_BAD_TABLE)
+    r.c.block_table.copy_(good)
+    # a plan that runs ahead of the rows' state
+    ahead = moba.CachePlan(plan.cu_new, plan.token_row, plan.token_pos + 1000, plan.slot_map)
+    out, lse = moba.cache_attention(r.c, ahead, q.cuda(), workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_BAD_TABLE and (out == 0).all() and torch.isinf(lse).all()
+    moba.cache_append(r.c, ahead, r.rand(n, 2, 64).cuda(), r.rand(n, 2, 64).cuda(), workspace=ws)
+    assert moba.check_status(ws) == moba.STATUS_BAD_TABLE
+    r.check_store()
+
+
+@gpu
+def test_offsets_beyond_32_bits():
+    """Pages whose bytes lie past 2^32 in the 8-bit buffers."""
+    B, h, d = 128, 8, 128
+    n_pages = 34000                                                   # 4.46 GB of keys, as much of values
+    r = Run(2, 40, 12, 16, h, d, B, "e4m3", 0, 3, seed=6)
+    c = moba.alloc_cache(2, n_pages, 12, h, d, B)
+    c.free_pages.copy_(torch.arange(n_pages - 1, -1, -1, dtype=torch.int32))
+    r.c, r.check = c, False
+    r.ref = cr.RefCache(2, n_pages, 12, h, d, B, "e4m3", 0)
+    r.ref.free = cr.deque(range(n_pages - 1, -1, -1))
+    for new in ([300, 129], [1, 1], [40, 0]):
+        plan, want, st = r.tables(new)
+        assert st == 0 and r.append(plan, want) == 0
+        ks = c.k_scale
+        for i in range(2):                                            # (check_store copies whole buffers: not these)
+            for j in range(r.ref.length[i] // B):
+                pg = r.ref.pages[i][j]
+                code, s = r.ref.block(r.ref.key, i, j)
+                assert torch.equal(ks[pg].cpu(), s)
+                assert torch.equal(c.k[pg].cpu().float(), code.float())
+                r.ref.cents[pg] = c.cent[0, pg].cpu().double() + c.cent[1, pg].cpu().double()
+        r.queries(plan, want)
+
+
+# ---------------------------------------------------------------------------------------------- streams, graphs, the ABI
+@gpu
+def test_a_generation_step_replays_from_a_graph():
+    """One captured step (tables in place, append, route, attention) generates token after token."""
+    rows, hq, h, d, B, W, topk = 3, 4, 2, 64, 16, 4, 3
+    r = Run(rows, 60, 20, hq, h, d, B, "e4m3", W, topk, seed=8)
+    r.step([50, 17, 0])
+    new = torch.ones(rows, dtype=torch.int32, device="cuda")
+    k, v, q = (torch.zeros((rows, n, d), dtype=torch.bfloat16, device="cuda") for n in (h, h, hq))
+    w = r.w.cuda()
+    ws = r.c.alloc_workspace(rows, hq)
+    state = {n: getattr(r.c, n).clone() for n in ("k", "v", "k_scale", "v_scale", "cent", "tail_k", "tail_v", "hist",
+                                                 "block_table", "row_state", "free_pages", "ring")}
+
+    def step():
+        plan = moba.cache_tables(r.c, new, rows, workspace=ws)
+        moba.cache_append(r.c, plan, k, v, conv_w=w, workspace=ws)
+        sel = moba.cache_route(r.c, plan, q, topk, workspace=ws)
+        return (plan, sel) + moba.cache_attention(r.c, plan, q, sel_idx=sel, workspace=ws) + \
+            moba.cache_attention(r.c, plan, q, workspace=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan, sel, out, lse, out_all, lse_all = step()
+    for n, x in state.items():                                        # the warm-up step is taken back
+        getattr(r.c, n).view(torch.uint8).copy_(x.view(torch.uint8))
+    for i in range(20):
+        kk, vv, qq = r.rand(rows, h, d), r.rand(rows, h, d), r.rand(rows, hq, d)
+        for x, y in ((k, kk), (v, vv), (q, qq)):
+            x.copy_(y)
+        new.copy_(torch.tensor([1, i % 2, 1]))                         # a row that rests every other step
+        graph.replay()
+        want = r.ref.tables([1, i % 2, 1], rows)
+        for got, exp in zip(plan, want):
+            assert got.tolist() == exp
+        r.ref.append(want[0], want[4], kk[:], vv, r.w)
+        r.check_store()
+        n = want[0][-1]
+        exp = r.ref.route(want[1], want[2], qq, topk)
+        assert torch.equal(sel.cpu()[:n], exp[:n])
+        for o, l, e in ((out, lse, exp), (out_all, lse_all, None)):
+            ref = r.ref.attend(want[1], want[2], qq, e)
+            cr.check_attention(o.cpu()[:n], l.cpu()[:n], [x[:n] for x in ref], d)
+    assert moba.check_status(ws) == 0
+
+
+@gpu
+def test_two_streams_with_a_workspace_each():
+    """Steps of two caches on two streams at once give what they give alone."""
+    a, b = (Run(2, 60, 40, 4, 1, 128, 16, kind, 0, 4, seed=i) for i, kind in enumerate(("e4m3", "int8")))
+    jobs = []
+    for r in (a, b):
+        plan, want, _ = r.tables([300, 100])
+        r.append(plan, want)
+        plan, want, _ = r.tables([90, 1])
+        r.append(plan, want)
+        jobs.append((r, plan, want, r.rand(91, 4, 128)))
+    alone = []
+    for r, plan, want, q in jobs:
+        ws = r.c.alloc_workspace(91, 4)
+        sel = moba.cache_route(r.c, plan, q.cuda(), 4, workspace=ws)
+        alone.append([x.clone() for x in (sel,) + moba.cache_attention(r.c, plan, q.cuda(), sel_idx=sel) + moba.cache_attention(r.c, plan, q.cuda())])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    qs = [q.cuda() for _, _, _, q in jobs]
+    torch.cuda.synchronize()
+    got = []
+    for rep in range(5):
+        got = []
+        for (r, plan, _, _), q, s in zip(jobs, qs, streams):
+            with torch.cuda.stream(s):
+                sel = moba.cache_route(r.c, plan, q, 4)
+                got.append((sel,) + moba.cache_attention(r.c, plan, q, sel_idx=sel) + moba.cache_attention(r.c, plan, q))
+        torch.cuda.synchronize()
+        for x, y in zip(got, alone):
+            for u, w in zip(x, y):
+                assert torch.equal(u, w)
+
+
+@gpu
+def test_binding_refuses_what_does_not_fit():
+    c = moba.alloc_cache(2, 10, 4, 2, 64, 16, conv_width=3)
+    new = torch.ones(2, dtype=torch.int32, device="cuda")
+    plan = moba.cache_tables(c, new, 2)
+    ok = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 64, 3), device="cuda")
+    with pytest.raises(TypeError):
+        moba.cache_append(c, plan, ok.float(), ok, conv_w=w)
+    with pytest.raises(ValueError):
+        moba.cache_append(c, plan, ok[:1], ok, conv_w=w)
+    with pytest.raises(ValueError):
+        moba.cache_append(c, plan, torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")[:, ::2], ok, conv_w=w)
+    with pytest.raises(ValueError):
+        moba.cache_append(c, plan, ok, ok)
+    with pytest.raises(ValueError):
+        moba.cache_append(c, plan, ok, ok, conv_w=w[..., :2].contiguous())
+    with pytest.raises(TypeError):
+        moba.cache_tables(c, new.long(), 2)
+    with pytest.raises(ValueError):
+        moba.cache_tables(c, new[:1], 2)
+    with pytest.raises(ValueError):
+        moba.cache_tables(c, new, -1)
+    with pytest.raises(ValueError):
+        moba.cache_tables(c, new, 3, plan=plan)
+    with pytest.raises(TypeError):
+        moba.cache_route(c, tuple(plan), ok, 2)
+    with pytest.raises(ValueError):
+        moba.cache_route(c, plan, torch.zeros((2, 2, 128), dtype=torch.bfloat16, device="cuda"), 2)
+    for hq, topk in ((3, 2), (2, 0), (2, 65)):
+        with pytest.raises((moba.MobaError, RuntimeError)):
+            moba.cache_route(c, plan, torch.zeros((2, hq, 64), dtype=torch.bfloat16, device="cuda"), topk)
+    with pytest.raises(moba.MobaError):
+        moba.cache_route(c, plan, ok, 2, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        moba.cache_attention(c, plan, ok, sel_idx=torch.zeros((1, 2, 2), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        moba.cache_attention(c, plan, ok, lse=torch.zeros((2, 3), device="cuda"))
+    other = moba.alloc_cache(3, 10, 4, 2, 64, 16)
+    with pytest.raises(ValueError):
+        moba.cache_attention(other, plan, ok)
+    # nothing to do is no error
+    none = moba.cache_tables(c, torch.zeros_like(new), 0)
+    empty = ok[:0]
+    moba.cache_append(c, none, empty, empty, conv_w=w)
+    assert moba.cache_route(c, none, empty, 2).shape == (0, 2, 2)
+    assert moba.cache_attention(c, none, empty)[0].shape == (0, 2, 64)
+
+
+@gpu
+@pytest.mark.parametrize("W", [0, 4])
+def test_cached_routing_agrees_with_the_prompt_path(W):
+    """The same prompt through moba.forward and through the cache: the centroids are the same but for the order of 32-bit
+    sums, so selections differ in near ties only."""
+    from block_sparse_long_key_b200 import synth
+    w = synth.small((700, 333), 4, 2, 64, 32, 6, conv_width=W, seed=4)
+    x = {n: (t.cuda() if isinstance(t, torch.Tensor) else t) for n, t in synth.make_inputs(w, with_dout=False).items()}
+    out, lse, sel, _ = moba.forward(x["q"], x["k"], x["v"], x["cu_seqlens"], 32, 6, conv_w=x.get("conv_w"))
+    c = moba.alloc_cache(2, 40, 30, 2, 64, 32, conv_width=W)
+    plan = moba.cache_tables(c, torch.tensor([700, 333], dtype=torch.int32, device="cuda"), 1033)
+    moba.cache_append(c, plan, x["k"], x["v"], conv_w=x.get("conv_w"))
+    got = moba.cache_route(c, plan, x["q"], 6)
+    same = (got == sel).all(-1)
+    assert same.float().mean() > 0.999
+    o, l = moba.cache_attention(c, plan, x["q"], sel_idx=got)
+    # e4m3 keeps keys to 2^-4: scores move by about 2^-4 / sqrt(3) / sqrt(64) |q| |k| ~ 0.04 rms, outputs likewise
+    d = (o.float() - out.float())[same]
+    assert d.pow(2).mean().sqrt() < 0.1 * out.float().pow(2).mean().sqrt()
+    assert (l - lse)[same].abs().max() < 0.5
