@@ -163,7 +163,6 @@ int moba_cache_route(const moba_cache* cache, const moba_cache_plan* plan, const
   if ((rc = check_ws(workspace, workspace_bytes, workspace_need(cache, plan->total_new, h_q))) != MOBA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  MOBA_TRY(cudaMemsetAsync(ws, 0, 2 * sizeof(int32_t), st));
   MOBA_TRY(moba::cache::launch_route(view_of(cache), plan_of(plan), static_cast<const bf16*>(q), h_q, topk, sel_idx,
                                      ws + kAlign, reinterpret_cast<int32_t*>(ws), st));
   return MOBA_OK;

@@ -56,19 +56,25 @@ __device__ __forceinline__ int own_block(const View& c, int row, int pos) {
   return pos < c.state[2 * row] && j < c.state[2 * row + 1] ? j : -2;
 }
 
-template <int D>
+// SHARE: the CTA's warps take the blocks of one tile in turn; else each has a tile of its own, and neighbours (mostly of
+// one request) find one another's centroids in L1.
+template <int D, bool SHARE>
 __global__ void __launch_bounds__(kScoreThreads)
 score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float* __restrict__ score,
              float* __restrict__ hmax, int32_t* status) {
-  constexpr int NT = 4;  // n-tiles (of 8 blocks) per warp and step
-  __shared__ __align__(16) bf16 qs[16 * (D + 8)];
-  __shared__ float smax[kScoreThreads / 32];
+  constexpr int NT = 4, WARPS = kScoreThreads / 32;  // n-tiles (of 8 blocks) per warp and step
+  __shared__ __align__(16) bf16 qbuf[(SHARE ? 1 : WARPS) * 16 * (D + 8)];
+  __shared__ float smax[WARPS];
+  cudaTriggerProgrammaticLaunchCompletion();  // select_kernel may start; it waits for this grid's end where it has to
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int G = h_q / c.h_kv, head = blockIdx.y, u = blockIdx.x;
+  if (sl.t0 == 0 && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) status[0] = status[1] = 0;
+  const int G = h_q / c.h_kv, head = blockIdx.y, u = SHARE ? blockIdx.x : blockIdx.x * WARPS + warp;
+  bf16* qs = qbuf + (SHARE ? 0 : warp * 16 * (D + 8));
   int row, tok0, r0, nrows;
   if (sl.per_token) {
     const int tiles = (G + 15) / 16;
     tok0 = sl.t0 + u / tiles;
+    if (tok0 >= sl.t1) return;
     row = __ldg(p.row + tok0);
     if ((unsigned)row >= (unsigned)c.rows) return;
     r0 = (u % tiles) * 16;
@@ -94,13 +100,13 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
   const size_t at_max = ((size_t)u * c.h_kv + head) * sl.nchunk + blockIdx.z;
   if (j0 >= j1) return;
   auto item_of = [&](int r) { return (size_t)(tok0 + (r0 + r) / G) * h_q + head * G + (r0 + r) % G; };
-  for (int i = tid; i < 16 * (D / 8); i += kScoreThreads) {
+  for (int i = SHARE ? tid : lane; i < 16 * (D / 8); i += SHARE ? kScoreThreads : 32) {
     const int r = i / (D / 8), ck = i % (D / 8);
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < rows) x = *reinterpret_cast<const uint4*>(q + item_of(r) * D + ck * 8);
     *reinterpret_cast<uint4*>(qs + r * (D + 8) + ck * 8) = x;
   }
-  __syncthreads();
+  if constexpr (SHARE) __syncthreads(); else __syncwarp();
   // Lane's share of a row: channels 64 hh + 16 t .. + 15; k-step x of a half takes 4 of them.
   uint32_t qf[D / 16][4];
 #pragma unroll
@@ -114,12 +120,14 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
 #pragma unroll
   for (int r = 0; r < 2; ++r)
     dst[r] = g + 8 * r < rows ? score + (item_of(g + 8 * r) - (size_t)sl.t0 * h_q) * sl.stride + 2 * t : nullptr;
-  for (int j = j0 + warp * NT * 8; j < j1; j += kScoreThreads / 32 * NT * 8) {
-    int mine = -1;
-    if (j + lane < j1) {
-      mine = block_page(c, row, j + lane);
-      if (mine < 0) set_status(status, kStatusBadTable);
-    }
+  constexpr int STEP = (SHARE ? WARPS : 1) * NT * 8;
+  const int first = j0 + (SHARE ? warp * NT * 8 : 0);
+  auto page_at = [&](int j) { return j < j1 ? __ldg(c.table + (size_t)row * c.max_blocks + j) : 0; };
+  int next = page_at(first + lane);
+  for (int j = first; j < j1; j += STEP) {
+    const int mine = (unsigned)next < (unsigned)c.n_pages ? next : -1;
+    if (j + lane < j1 && mine < 0) most = CUDART_NAN_F;  // no such page: the row is looked at block by block
+    next = page_at(j + STEP + lane);
     uint4 w[NT][D / 64][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -128,7 +136,8 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) w[n][hh][x] = pg >= 0 ? __ldg(src + hh * 8 + x) : make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < 2; ++x)
+          w[n][hh][x] = pg >= 0 && j + n * 8 + g < j1 ? __ldg(src + hh * 8 + x) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -147,7 +156,7 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
       }
       sq += __shfl_xor_sync(~0u, sq, 1);
       sq += __shfl_xor_sync(~0u, sq, 2);
-      most = sq > most || sq != sq ? sq : most;
+      most = sq > most || sq != sq ? sq : most;  // NaN stays (nothing compares with it)
       const int jj = j + n * 8 + 2 * t;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -157,14 +166,18 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
         }
     }
   }
-  for (int off = 4; off < 32; off <<= 1) {
+  for (int off = 1; off < 32; off <<= 1) {
     const float o = __shfl_xor_sync(~0u, most, off);
     most = o > most || o != o ? o : most;
   }
-  if (lane == 0) smax[warp] = most;
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kScoreThreads / 32; ++i) most = smax[i] > most || smax[i] != smax[i] ? smax[i] : most;
+  if constexpr (SHARE) {
+    if (lane == 0) smax[warp] = most;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < WARPS; ++i) most = smax[i] > most || smax[i] != smax[i] ? smax[i] : most;
+      hmax[at_max] = most;
+    }
+  } else if (lane == 0) {
     hmax[at_max] = most;
   }
 }
@@ -190,19 +203,20 @@ struct List {
   int j[kCand];
   int todo[kCand];         // list positions of the candidates being scored,
   int page[kCand];         // their pages, then the upper words of their exact scores
-  int count;
 };
 
 // 64-bit scores of the candidates i < n for which `want(i)`, 16 at a time (2 lanes each); their list positions stay in
 // todo, the upper words of their scores in page; returns their number.
 template <int D, typename F>
-__device__ __forceinline__ int rescore(const View& c, int row, int head, const bf16* q, List& ls, int n, F want) {
+__device__ __forceinline__ int rescore(const View& c, int row, int head, const bf16* q, List& ls, int n,
+                                       int32_t* status, F want) {
   constexpr int V = D / 16;  // 16-byte pieces per lane
   const int lane = threadIdx.x & 31, sub = lane & 1;
   int m = 0;
   for (int x = 0; x < n; x += 32) {
     const bool w = x + lane < n && want(x + lane);
     const int pg = w ? block_page(c, row, ls.j[x + lane]) : -1;
+    if (w && pg < 0) set_status(status, kStatusBadTable);
     const uint32_t b = __ballot_sync(~0u, w);
     const int at = m + __popc(b & ((1u << lane) - 1));
     if (w) ls.todo[at] = x + lane, ls.page[at] = pg;
@@ -258,7 +272,7 @@ __device__ __forceinline__ bool among(const List& ls, const int* todo, int m, in
 // in the list; all have their exact scores.
 template <int D>
 __device__ __noinline__ int many_candidates(const View& c, int row, int head, const bf16* q, List& ls, const float* sc,
-                                            int own, float bar, int K) {
+                                            int own, float bar, int K, int32_t* status) {
   const int lane = threadIdx.x & 31;
   int n = 0, scored = 0;
   for (int base = 0; base < own; base += 32) {
@@ -269,7 +283,7 @@ __device__ __noinline__ int many_candidates(const View& c, int row, int head, co
     n += __popc(m);
     __syncwarp();
     if (n > kCand - 32) {
-      rescore<D>(c, row, head, q, ls, n, [&](int i) { return i >= scored; });
+      rescore<D>(c, row, head, q, ls, n, status, [&](int i) { return i >= scored; });
       uint32_t keep = 0;  // ranks need the whole list: first all of them, then the moves
       for (int x = 0; x * 32 < n; ++x) {
         const int i = x * 32 + lane;
@@ -291,7 +305,7 @@ __device__ __noinline__ int many_candidates(const View& c, int row, int head, co
       n = scored = kept;
     }
   }
-  rescore<D>(c, row, head, q, ls, n, [&](int i) { return i >= scored; });
+  rescore<D>(c, row, head, q, ls, n, status, [&](int i) { return i >= scored; });
   return n;
 }
 
@@ -334,6 +348,7 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
   if ((unsigned)row >= (unsigned)c.rows) return;
   int32_t* out = sel + item * topk;
   const int own = own_block(c, row, pos);
+  cudaGridDependencySynchronize();  // the screen scores are there
   const int K = topk - 1;
   if (own <= K) {  // every earlier block; none (-1) for a token that sees nothing
     if (own == -2 && lane == 0) set_status(status, kStatusBadTable);
@@ -409,15 +424,8 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
     }
   }
   // ---- candidates, in no order: pieces with one as bits, then those pieces once more
-  if (lane == 0) ls.count = 0;
-  __syncwarp();
+  int n = 0;
   if (!odd) {
-    auto add = [&](float s, int j) {
-      if (s >= bar) {
-        const int at = atomicAdd(&ls.count, 1);
-        if (at < kCand) ls.screen[at] = s, ls.j[at] = j;
-      }
-    };
     for (int base = 0; base < own; base += kHeld * 128) {
       uint32_t hit = 0;
       if (own <= kHeld * 128) {
@@ -430,20 +438,33 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
           hit |= (uint32_t)(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= bar) << r;
         }
       }
-      while (hit) {
+      while (__any_sync(~0u, hit)) {
         const int j = base + 128 * (__ffs(hit) - 1) + 4 * lane;
+        float4 v = make_float4(kNone, kNone, kNone, kNone);
+        if (hit) v = piece(j);
         hit &= hit - 1;
-        const float4 v = piece(j);
-        add(v.x, j), add(v.y, j + 1), add(v.z, j + 2), add(v.w, j + 3);
+        const float s[4] = {v.x, v.y, v.z, v.w};
+        int at = n;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t m = __ballot_sync(~0u, s[x] >= bar);
+          at += __popc(m & ((1u << lane) - 1));
+          n += __popc(m);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (s[x] >= bar) {
+            if (at < kCand) ls.screen[at] = s[x], ls.j[at] = j + x;
+            ++at;
+          }
       }
     }
     __syncwarp();
   }
-  int n = ls.count;
   // picks: this lane's list positions lane + 32 x, as bits
   uint32_t picks = 0;
   if (odd || n > kCand) {
-    n = many_candidates<D>(c, row, head, qr, ls, sc, own, odd ? -CUDART_INF_F : bar, K);
+    n = many_candidates<D>(c, row, head, qr, ls, sc, own, odd ? -CUDART_INF_F : bar, K, status);
     for (int x = 0; x * 32 < n; ++x) {
       const int i = x * 32 + lane;
       if (i < n && among(ls, nullptr, n, K, ls.exact[i], ls.j[i])) picks |= 1u << x;
@@ -464,7 +485,7 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
         is_sure |= (uint32_t)s << x;
         n_sure += __popc(__ballot_sync(~0u, s));
       }
-    const int m = rescore<D>(c, row, head, qr, ls, n, [&](int i) { return !(is_sure >> (i >> 5) & 1); });
+    const int m = rescore<D>(c, row, head, qr, ls, n, status, [&](int i) { return !(is_sure >> (i >> 5) & 1); });
     picks = is_sure;
     // the ones in doubt, two per lane, against all of them: by the upper words of their scores, where those decide
     for (int first = 0; first < m; first += 64) {
@@ -533,17 +554,51 @@ int slab_tokens(const View& c, int T, int h_q) {
   return (int)(n < 1 ? 1 : (n < T ? n : T));
 }
 
-int chunk_of(const View&) { return 256; }
+// Blocks per CTA of kernel one: the more, the less a tile's look-ups cost, as long as 8 CTAs per SM remain (64 rows of
+// ragged length up to 2048 blocks: 30 us with 256 blocks, 19 with 1024; one row: 6 and 5 us with 256 and 128).
+int chunk_of(const View& c, int slab, int h_q) {
+  int per_token;
+  const long long tiles = tiles_of(c, slab, h_q, &per_token) * c.h_kv / (per_token ? 1 : kScoreThreads / 32);
+  int chunk = 128;
+  while (chunk < 1024 && tiles * ((c.max_blocks + 2 * chunk - 1) / (2 * chunk)) >= 8 * 148) chunk *= 2;
+  while ((c.max_blocks + chunk - 1) / chunk > 65535) chunk *= 2;
+  return chunk;
+}
+
+template <int D>
+cudaError_t launch_slab(const View& c, const Plan& p, const Slab& sl, long long tiles, const bf16* q, int h_q, int topk,
+                        float* score, float* hmax, int32_t* sel, int32_t* status, cudaStream_t st) {
+  constexpr int WARPS = kScoreThreads / 32;
+  if (sl.per_token) {
+    const dim3 grid((unsigned)tiles, c.h_kv, sl.nchunk);
+    score_kernel<D, true><<<grid, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
+  } else {
+    const dim3 grid((unsigned)((tiles + WARPS - 1) / WARPS), c.h_kv, sl.nchunk);
+    score_kernel<D, false><<<grid, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((long long)(sl.t1 - sl.t0) * h_q + kSelWarps - 1) / kSelWarps));
+  cfg.blockDim = dim3(kSelWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, select_kernel<D>, c, p, sl, q, h_q, topk, (const float*)score, (const float*)hmax, sel,
+                            status);
+}
 
 }  // namespace
 
 size_t route_scratch(const View& c, int T, int h_q) {
   if (T == 0) return 0;
-  const int n = slab_tokens(c, T, h_q);
+  const int n = slab_tokens(c, T, h_q), chunk = chunk_of(c, n, h_q);
   int per_token;
-  const long long tiles = tiles_of(c, n, h_q, &per_token);
-  const int nchunk = (c.max_blocks + chunk_of(c) - 1) / chunk_of(c);
-  return ((size_t)n * h_q * stride_of(c) + (size_t)tiles * c.h_kv * nchunk) * sizeof(float);
+  const long long tiles = tiles_of(c, n, h_q, &per_token) + kScoreThreads / 32;
+  return ((size_t)n * h_q * stride_of(c) + (size_t)tiles * c.h_kv * ((c.max_blocks + chunk - 1) / chunk)) * sizeof(float);
 }
 
 cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, int topk, int32_t* sel, void* scratch,
@@ -555,19 +610,11 @@ cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, i
     Slab sl;
     sl.t0 = t0, sl.t1 = t0 + step < p.T ? t0 + step : p.T;
     const long long tiles = tiles_of(c, sl.t1 - t0, h_q, &sl.per_token);
-    sl.chunk = chunk_of(c);
+    sl.chunk = chunk_of(c, step, h_q);
     sl.nchunk = (c.max_blocks + sl.chunk - 1) / sl.chunk;
     sl.stride = stride_of(c);
-    const dim3 g1((unsigned)tiles, c.h_kv, sl.nchunk);
-    const unsigned g2 = (unsigned)(((long long)(sl.t1 - t0) * h_q + kSelWarps - 1) / kSelWarps);
-    if (c.d == 64) {
-      score_kernel<64><<<g1, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
-      select_kernel<64><<<g2, kSelWarps * 32, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
-    } else {
-      score_kernel<128><<<g1, kScoreThreads, 0, st>>>(c, p, sl, q, h_q, score, hmax, status);
-      select_kernel<128><<<g2, kSelWarps * 32, 0, st>>>(c, p, sl, q, h_q, topk, score, hmax, sel, status);
-    }
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = c.d == 64 ? launch_slab<64>(c, p, sl, tiles, q, h_q, topk, score, hmax, sel, status, st)
+                                    : launch_slab<128>(c, p, sl, tiles, q, h_q, topk, score, hmax, sel, status, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
