@@ -419,45 +419,63 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
       const float4* prm = reinterpret_cast<const float4*>(sm + Ly::UNIT_OFF + (i & 1) * kUnits * 16);
       const int nvis = min(kKeys, min(pos + 1, kend) - (kt0 + i) * kKeys);  // visible keys of this row, from the first
       uint32_t s[2][32];  // scores; from its start on, pairs of weights take their place
-      tc::tmem_ld32(tm_s, s[0]);
-      tc::tmem_ld32(tm_s + 32, s[1]);
-      tc::tmem_ld_wait();
-      if (!__all_sync(~0u, nvis == kKeys)) {
+      auto load = [&]() {
+        tc::tmem_ld32(tm_s, s[0]);
+        tc::tmem_ld32(tm_s + 32, s[1]);
+        tc::tmem_ld_wait();
+        if (!__all_sync(~0u, nvis == kKeys)) {
 #pragma unroll
-        for (int x = 0; x < kKeys; ++x)
-          if (x >= nvis) s[x / 32][x % 32] = 0xff800000u;
-      }
-      constexpr int NU = ONE ? 1 : kUnits, UK = kKeys / NU;  // groups of keys under one pair of scales
-      float top[NU];  // largest score of each
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        float t[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) t[x] = __uint_as_float(s[(u * UK + x) / 32][(u * UK + x) % 32]);
-#pragma unroll
-        for (int x = 4; x < UK; ++x) t[x & 3] = fmaxf(t[x & 3], __uint_as_float(s[(u * UK + x) / 32][(u * UK + x) % 32]));
-        top[u] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-      }
+          for (int x = 0; x < kKeys; ++x)
+            if (x >= nvis) s[x / 32][x % 32] = 0xff800000u;
+        }
+      };
+      load();
       // the units' scales come with the V tile
       if (!__all_sync(~0u, got(mb_v, i))) { *fail = 1; break; }
-      float mx = -CUDART_INF_F, f1[NU], b1[NU], inv[NU], rest[NU];
-      bool odd = false;  // a V scale below 2^-100
+      constexpr int NU = ONE ? 1 : kUnits, UK = kKeys / NU;  // groups of keys under one pair of scales
+      bool odd, ok = true;  // odd: a V scale below 2^-100
+      // Weights under the reference as it is, and the tile's maximum beside them (the exponentials leave room for it).
+      // Where a row's maximum has outgrown its reference, which is seldom, the reference is moved and the tile done again.
+      while (true) {
+        const float off = kOffset - (m == -CUDART_INF_F ? 0.f : m);
+        float mx = -CUDART_INF_F, add = 0.f;
+        odd = false;
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        const float4 pr = prm[u];
-        // at least 2^-120, so that -infinity stays itself; smaller factors meet scores that they make zero anyway
-        f1[u] = fmaxf(fac * pr.x, 7.5231639e-37f);
-        b1[u] = pr.y, rest[u] = pr.z, inv[u] = pr.w;
-        mx = fmaxf(mx, fmaf(top[u], f1[u], pr.y));
-        odd |= pr.z != 1.f;
-      }
-      const bool up = mx > m + kSlack;  // m = -infinity: any
-      if (__any_sync(~0u, up)) {
+        for (int u = 0; u < NU; ++u) {
+          const float4 pr = prm[u];
+          // at least 2^-120, so that -infinity stays itself; smaller factors meet scores that they make zero anyway
+          const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f);
+          const uint64_t f = pair(f1, f1), b = pair(pr.y + off, pr.y + off);
+          uint64_t sum[2] = {0, 0};  // two zeros each
+          float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+          for (int x = 0; x < UK; x += 2) {
+            const int k = u * UK + x;
+            const float s0 = __uint_as_float(s[k / 32][k % 32]), s1 = __uint_as_float(s[k / 32][k % 32 + 1]);
+            float e0, e1;
+            unpair(fma2(pair(s0, s1), f, b), e0, e1);
+            top[0] = fmaxf(top[0], s0), top[1] = fmaxf(top[1], s1);
+            e0 = fast_exp2(e0), e1 = fast_exp2(e1);
+            sum[x / 2 & 1] = add2(sum[x / 2 & 1], pair(e0, e1));
+            s[0][k / 2] = pack_f16(e0, e1);
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(top[0], top[1]), f1, pr.y));
+          float s0, s1;
+          unpair(add2(sum[0], sum[1]), s0, s1);
+          add = fmaf(s0 + s1, pr.w, add);
+          odd |= pr.z != 1.f;
+        }
+        const bool up = mx > m + kSlack;  // m = -infinity: any
+        if (!__any_sync(~0u, up)) {
+          l += add;
+          break;
+        }
         const float a = up ? fast_exp2(m - mx) : 1.f;
         if (up) m = mx;
         l *= a;
         if (i > 0) {
-          if (!__all_sync(~0u, got(mb_o, i - 1))) { *fail = 1; break; }
+          ok = __all_sync(~0u, got(mb_o, i - 1));
+          if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll 1
           for (int h = 0; h < D / 16; ++h) {
@@ -469,26 +487,13 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
             tmem_st16(tmem + lane_base + Ly::TM_O + h * 16, o);
           }
         }
+        load();
       }
-      const float off = kOffset - (m == -CUDART_INF_F ? 0.f : m);
+      if (!ok) { *fail = 1; break; }
+      if (__any_sync(~0u, odd)) {
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        const uint64_t f = pair(f1[u], f1[u]), b = pair(b1[u] + off, b1[u] + off);
-        uint64_t sum[2] = {0, 0};  // two zeros each
-#pragma unroll
-        for (int x = 0; x < UK; x += 2) {
-          const int k = u * UK + x;
-          float e0, e1;
-          unpair(fma2(pair(__uint_as_float(s[k / 32][k % 32]), __uint_as_float(s[k / 32][k % 32 + 1])), f, b), e0, e1);
-          e0 = fast_exp2(e0), e1 = fast_exp2(e1);
-          sum[x / 2 & 1] = add2(sum[x / 2 & 1], pair(e0, e1));
-          s[0][k / 2] = pack_f16(e0, e1);
-        }
-        float s0, s1;
-        unpair(add2(sum[0], sum[1]), s0, s1);
-        l = fmaf(s0 + s1, inv[u], l);
-        if (odd) {
-          const __half2 z = __float2half2_rn(rest[u]);
+        for (int u = 0; u < NU; ++u) {
+          const __half2 z = __float2half2_rn(prm[u].z);
 #pragma unroll
           for (int x = 0; x < UK / 2; ++x) {
             __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][u * UK / 2 + x]), z);
