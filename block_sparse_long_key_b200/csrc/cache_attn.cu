@@ -5,19 +5,21 @@
 // Arithmetic.  An 8-bit code (e4m3 or int8) is exactly an fp16 value, so a page
 // is multiplied as fp16 with fp32 sums and the block's scales stay outside:
 // ks scales the score, vs is carried in the exponent.  With
-//   x_i = s_i log2 e + log2 vs,   M = running max of x_i,   w_i = 2^(x_i - M + 15)
-// the output is sum w_i v8_i / (2^15 l), l = sum w_i 2^-15 / vs = sum 2^(s_i log2 e - M),
-// and log2 of the softmax sum is M + log2 l.  So no block's product has to be
+//   x_i = s_i log2 e + log2 vs,   M >= max x_i - 8,   w_i = 2^(x_i - M + 7) <= 2^15
+// the output is sum w_i v8_i / (2^7 l), l = sum w_i 2^-7 / vs = sum 2^(s_i log2 e - M),
+// and log2 of the softmax sum is M + log2 l.  The reference M follows the
+// running maximum only when that has grown by more than 8, so in most steps
+// nothing is reduced across lanes or rescaled.  So no block's product has to be
 // scaled on its own, whatever the spread of the scales (vs is taken as at
 // least 2^-100, so that 1 / vs and l stay finite; the rest of a smaller scale
 // is multiplied into w_i).  Queries are fp16 after a power of two per row that
 // brings the row's largest magnitude to [2^8, 2^9): exact down to 2^-22 of
-// it.  Weights are rounded to fp16 (2^-11, the offset 2^15 keeps weights down
-// to 2^-29 of the largest out of the subnormals); their sum is kept in fp32
+// it.  Weights are rounded to fp16 (2^-11; those below 2^-21 of the one at the
+// reference are subnormal, with steps of 2^-31 of it); their sum is kept in fp32
 // from the unrounded ones.
 //
 // A partial block is bf16 (the tail) and is multiplied as bf16, its weights
-// 2^(s_i log2 e - M + 15) as hi + lo; in M it counts with its largest |v| / 448.
+// 2^(s_i log2 e - M + 7) as hi + lo; in M it counts with its largest |v| / 448.
 //
 // Fragments (mma.m16n8k16; lane = 4 g + t).  Keys come 16 tokens (a unit) at a
 // time and are the M side of both products, so that up to 8 query rows (the
@@ -39,7 +41,8 @@ namespace {
 
 constexpr int kUnit = 16;        // tokens per unit
 constexpr int kPair = 2;         // units per softmax step
-constexpr float kOffset = 15.f;  // exponent of the largest weight
+constexpr float kOffset = 7.f;   // exponent of a weight at the reference
+constexpr float kSlack = 8.f;    // growth of a row's maximum that leaves its reference alone
 constexpr int kListCap = 128;    // list entries held in shared memory at a time
 
 // ---------------------------------------------------------------- fragments
@@ -189,24 +192,21 @@ struct State {
         for (int x = 0; x < 4; ++x) o[n][i][x] = 0.f;
     }
   }
-  // Raises the references to cover mx (this lane's maxima over its tokens).
+  // Raises the references to mx (this lane's maxima over its tokens) where one has been outgrown by more than the slack.
   __device__ __forceinline__ void raise(float (*mx)[2]) {
     bool up = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) mx[n][b] = fmaxf(mx[n][b], __shfl_xor_sync(~0u, mx[n][b], off));
-        up |= mx[n][b] > m[n][b];
-      }
+    for (int n = 0; n < NT; ++n) up |= mx[n][0] > m[n][0] + kSlack || mx[n][1] > m[n][1] + kSlack;  // m = -inf: any
     if (__any_sync(~0u, up)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float a[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float x = fmaxf(m[n][b], mx[n][b]);
+          float x = mx[n][b];
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, off));
+          x = fmaxf(m[n][b], x);
           a[b] = x > m[n][b] ? fast_exp2(m[n][b] - x) : 1.f;  // m = -inf: 0
           m[n][b] = x;
           l[n][b] *= a[b];
@@ -232,14 +232,14 @@ struct __align__(16) Entry {
   float ks;
   float lv;      // log2 of the V scale, taken as at least 2^-100
   float rest;    // V scale over that (1 but for smaller scales)
-  float inv;     // 2^-15 over that
+  float inv;     // 2^-7 over that
   float pad;
 };
 
 __device__ __forceinline__ Entry make_entry(const View& c, int page, int j, int head) {
   const size_t at = (size_t)page * c.h_kv + head;
   const float s = __ldg(c.v_scale + at), vs = fmaxf(s, 7.8886090522101181e-31f);
-  return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 32768.f) / vs, 0.f};
+  return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 128.f) / vs, 0.f};
 }
 
 struct Tile {
@@ -325,7 +325,7 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
     }
   }
   st.raise(mx);
-  // weights 2^(s - M + 15): at most 2^(15 - lv), within bf16
+  // weights 2^(s - M + 7): at most 2^(15 - lv), within bf16
   uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -333,7 +333,7 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       s[n][x] = fast_exp2(s[n][x] - base[x & 1]);
-      st.l[n][x & 1] += s[n][x] * (1.f / 32768.f);
+      st.l[n][x & 1] += s[n][x] * (1.f / 128.f);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -681,7 +681,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     }
     const size_t item = item_of(r);
     if (nsplit == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / (32768.f * l);
+      const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
       uint2 y;
       y.x = pack_bf16(o[0] * inv, o[1] * inv), y.y = pack_bf16(o[2] * inv, o[3] * inv);
       *reinterpret_cast<uint2*>(out + item * D + ch) = y;
@@ -738,7 +738,7 @@ merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float*
     }
   }
   if constexpr (WARPS == 1) {
-    const float inv = l == 0.f ? 0.f : 1.f / (32768.f * l);
+    const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
 #pragma unroll
     for (int x = 0; x < E; ++x) out[item * D + lane + 32 * x] = __float2bfloat16_rn(l == 0.f ? 0.f : o[x] * inv);
     if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
@@ -758,7 +758,7 @@ merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float*
     l += a * sl[w];
     y += a * so[w][ch];
   }
-  out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (32768.f * l));
+  out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (128.f * l));
   if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
   }
 }

@@ -539,10 +539,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
           } else {
             float* b = part + (item * nsplit + split) * (D + 4);
 #pragma unroll
-            for (int x = 0; x < 16; x += 4)  // in units of cache_attn.cu's weights, 2^15
-              *reinterpret_cast<float4*>(b + h * 16 + x) =
-                  make_float4(__uint_as_float(o[x]) * 256.f, __uint_as_float(o[x + 1]) * 256.f,
-                              __uint_as_float(o[x + 2]) * 256.f, __uint_as_float(o[x + 3]) * 256.f);
+            for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4*>(b + h * 16 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
           }
         }
       }
