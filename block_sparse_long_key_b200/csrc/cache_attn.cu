@@ -365,7 +365,7 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
 // units in turn, each with its own ring of copies in flight, and are merged at
 // the end; with several splits the split's result goes to `part`.
 template <int D, int KIND, int NW, int NT, bool SEL>
-__global__ void __launch_bounds__(NW * 32, NW == 4 ? (D == 128 ? 3 : 4) : 1)
+__global__ void __launch_bounds__(NW * 32, NW <= 4 ? (D == 128 ? 12 : 16) / NW : 1)
 attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* __restrict__ sel, int topk,
             int per_token, int split_blocks, int nsplit, bf16* __restrict__ out, float* __restrict__ lse,
             float* __restrict__ part, int32_t* status) {
@@ -794,6 +794,10 @@ Cut cut_of(const View& c, int T, int h_q) {
   const long long least = (x.many ? 512 : 1024) / c.B;
   long long blocks = (c.max_blocks + want - 1) / want;
   if (blocks < least) blocks = least;
+  // a little more than one wave of CTAs (3 per SM at d = 128, 4 at 64) is worse than one of longer ones
+  const long long slots = (c.d == 128 ? 3 : 4) * 148, total = ctas * ((c.max_blocks + blocks - 1) / blocks);
+  if (!x.many && total > slots && total < 2 * slots && ctas <= slots)
+    blocks = (c.max_blocks + slots / ctas - 1) / (slots / ctas);
   blocks = (blocks + step - 1) / step * step;
   x.split_blocks = (int)blocks;
   x.nsplit = (int)((c.max_blocks + blocks - 1) / blocks);
@@ -818,9 +822,10 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
                        float* lse, float* part, int32_t* status, cudaStream_t st) {
   if (sel) {
     const dim3 grid(p.T, h_q);
-    // few rows: more warps each, so that their blocks are read at once
+    // Two warps a row leave the least to the last wave (1024 rows of 32 blocks of 32: 35 us with four, 31.7 with two,
+    // 33.6 with one); few rows take more, so that their blocks are read at once.
     if ((long long)p.T * h_q > 2 * 148)
-      return launch_one<D, KIND, 4, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
+      return launch_one<D, KIND, 2, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
     return launch_one<D, KIND, 8, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
   }
   const Cut x = cut_of(c, p.T, h_q);
