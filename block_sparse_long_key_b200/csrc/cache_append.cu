@@ -33,6 +33,10 @@ namespace moba {
 namespace cache {
 namespace {
 
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(smem)), "l"(gmem));
+}
+
 constexpr int kFewTokens = 4;  // see append_kernel
 constexpr int kDoubts = 512;   // roundings in doubt held per tile
 
@@ -153,18 +157,22 @@ __device__ __forceinline__ uint4* tail_at(bf16* tail, const View& c, int row, in
   return reinterpret_cast<uint4*>(tail + ((((size_t)row * 2 + (j & 1)) * c.h_kv + head) * c.B + off) * D + ch);
 }
 
-// Codes of 8 values x / s.  The quotient is x r with r = rn(1 / s), corrected
+// Codes of 8 values x / s, r = rn(1 / s).  The quotient is x r, corrected
 // once by its remainder (Markstein's correction step): within 2^-40 of half a
 // unit of its last place, so its rounding to 8 bits is the exact quotient's.
 // Scales where the remainder could leave the normal range are divided.
-template <int KIND>
-__device__ __forceinline__ uint2 encode8(uint4 u, float s, float r, bool divide) {
+template <int KIND, bool DIVIDE>
+__device__ __forceinline__ uint2 encode8(uint4 u, float s, float r) {
   float x[8];
   bf16x8_to_f32(u, x);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float y = x[e] * r;
-    x[e] = divide ? __fdiv_rn(x[e], s) : fmaf(fmaf(-y, s, x[e]), r, y);
+    if constexpr (DIVIDE) {
+      x[e] = __fdiv_rn(x[e], s);
+    } else {
+      const float y = x[e] * r;
+      x[e] = fmaf(fmaf(-y, s, x[e]), r, y);
+    }
   }
   uint2 o;
   if constexpr (KIND == 0) {
@@ -229,14 +237,29 @@ __device__ __forceinline__ float finite_amax(uint4* x, bool* bad) {
   return m;
 }
 
+template <int KIND>
+__device__ __noinline__ uint2 encode8_divide(uint4 u, float s) {
+  return encode8<KIND, true>(u, s, 0.f);
+}
+
 template <int KIND, int D, int BLK>
 __device__ __forceinline__ void write_codes(uint8_t* dst, const uint4* x, float s) {
   using S = Shape<D, BLK>;
   const float r = __frcp_rn(s);
-  const bool divide = s < 8.6736174e-19f;  // 2^-60
   dst += (threadIdx.x / S::LANES * S::NCH) * D + threadIdx.x % S::LANES * 8;
+  if (s < 8.6736174e-19f) {  // 2^-60
+#pragma unroll 1
+    for (int i = 0; i < S::NCH; ++i) {
+      uint4 u = x[0];
 #pragma unroll
-  for (int i = 0; i < S::NCH; ++i) *reinterpret_cast<uint2*>(dst + i * D) = encode8<KIND>(x[i], s, r, divide);
+      for (int k = 1; k < S::NCH; ++k)
+        if (k == i) u = x[k];
+      *reinterpret_cast<uint2*>(dst + i * D) = encode8_divide<KIND>(u, s);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S::NCH; ++i) *reinterpret_cast<uint2*>(dst + i * D) = encode8<KIND, false>(x[i], s, r);
+  }
 }
 
 template <int KIND>
@@ -361,6 +384,15 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     auto fetch = [&](int head) {
       if (head < head1) {
         uint4* dst = ring + ((head - head0) & 1) * S::STAGE + tid;
+        if (lo == 0 && hi == B) {  // a whole block of new tokens
+          const size_t at = ((size_t)(R.t_begin + rel0 + off0) * c.h_kv + head) * D + ch;
+          const size_t row = (size_t)c.h_kv * D;
+#pragma unroll
+          for (int i = 0; i < NCH; ++i) {
+            if (!CONV) cp_async16(dst + i * THREADS, k + at + i * row);
+            cp_async16(dst + (NCH + i) * THREADS, v + at + i * row);
+          }
+        } else {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
           const int off = off0 + i;
@@ -370,6 +402,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
           const void* vs = old ? (const void*)tail_at<D>(c.tail_v, c, R.row, j, head, off, ch) : (const void*)(v + at);
           if (!CONV || !fresh) cp_async16_zfill(dst + i * THREADS, ks, old || fresh);
           cp_async16_zfill(dst + (NCH + i) * THREADS, vs, old || fresh);
+        }
         }
         if constexpr (CONV) {  // raw keys of the new tokens and of the W - 1 before them
           uint4* rd = raws + ((head - head0) & 1) * S::RAW;
@@ -538,9 +571,11 @@ cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* 
   const int per_token = p.T <= runs;
   const long long n = per_token ? p.T : runs;
   // Heads one after the other in a CTA share its look-ups and overlap copies with rounding, as long as the GPU is
-  // filled (8 CTAs per SM).
-  long long per = n * c.h_kv / (8 * 148);
+  // filled (16 CTAs per SM), evenly.
+  long long per = n * c.h_kv / (16 * 148);
   per = per < 1 ? 1 : (per > c.h_kv ? c.h_kv : per);
+  const long long parts = (c.h_kv + per - 1) / per;
+  per = (c.h_kv + parts - 1) / parts;
   const dim3 grid((unsigned)n, (unsigned)((c.h_kv + per - 1) / per));
   cudaError_t e;
   if (c.conv_width > 0) {
