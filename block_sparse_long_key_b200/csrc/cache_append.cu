@@ -91,7 +91,8 @@ __device__ __forceinline__ float element(const uint4& u, int e) {
   return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
 }
 
-// k' of 8 channels of a token; tap(l): their raw keys l tokens before.  w: the head's weights [d, W]; ws: the same as [W, d] in shared memory, or null (a
+// k' of 8 channels of a token; tap(l): their raw keys l tokens before.  w: the head's weights [d, W]; ws: the same as [W, d] in shared memory, channels in the
+// order of wplace, or null (a
 // lane's 8 x W weights are then read one by one, which a CTA that converts many tokens would feel).
 // `doubt(e)` takes note of a channel whose rounding 32 bits do not settle and returns true, or returns false: then it is
 // settled here.
@@ -111,8 +112,8 @@ __device__ __forceinline__ uint4 conv8(int W, const float* w, const float* ws, i
       float x[8], wl[8];
       bf16x8_to_f32(raw[l], x);
       if (ws) {
-        *reinterpret_cast<float4*>(wl) = *reinterpret_cast<const float4*>(ws + l * D + ch);
-        *reinterpret_cast<float4*>(wl + 4) = *reinterpret_cast<const float4*>(ws + l * D + ch + 4);
+        *reinterpret_cast<float4*>(wl) = *reinterpret_cast<const float4*>(ws + l * D + ch / 2);
+        *reinterpret_cast<float4*>(wl + 4) = *reinterpret_cast<const float4*>(ws + l * D + D / 2 + ch / 2);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) wl[e] = __ldg(wc + e * W + l);
@@ -427,7 +428,8 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
 #pragma unroll
     for (int i = 0; i < NWR; ++i) {
       const int at = tid + i * THREADS, W = CONV ? c.conv_width : 1;
-      wplace[i] = at < D * W ? at % W * D + at / W : -1;
+      const int cc = at / W;  // of 8 channels the first 4 and the last 4 apart, so that neighbours read side by side
+      wplace[i] = at < D * W ? at % W * D + (cc >> 2 & 1) * (D / 2) + (cc >> 3) * 4 + (cc & 3) : -1;
     }
     auto ask_weights = [&](int head) {
       if constexpr (CONV) {
