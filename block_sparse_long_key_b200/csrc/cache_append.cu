@@ -315,6 +315,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     R.pos0 = __ldg(p.pos + R.t_begin);
     if (R.pos0 < 0) return;
     const int i = u - (R.t_begin / B + 2 * lo);  // number of the block among the row's touched ones
+    if (i < 0) return;
     first_rel = i == 0 ? 0 : (R.pos0 / B + i) * B - R.pos0;
   }
   R.n = min(end, min(total, p.T)) - R.t_begin;

@@ -412,7 +412,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       T.t0 = __ldg(p.cu + lo);
       T.r0 = (int)(u - ((long long)T.t0 * G / TR + lo)) * TR;
       T.nrows = (min(__ldg(p.cu + lo + 1), p.T) - T.t0) * G;
-      if (T.r0 >= T.nrows) return;
+      if (T.t0 < 0 || T.r0 < 0 || T.r0 >= T.nrows) return;
     }
   }
   const int len = c.state[2 * T.row], held = c.state[2 * T.row + 1];

@@ -182,15 +182,16 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const int row = lo, t0 = __ldg(p.cu + row);
   const int r0 = (int)(u0 - ((long long)t0 * G / kRows + row)) * kRows;
   const int nrows = (min(__ldg(p.cu + row + 1), p.T) - t0) * G;
-  if (r0 >= nrows) return;
+  if (t0 < 0 || r0 < 0 || r0 >= nrows) return;
   const int rows = min(kRows, nrows - r0);
   const int len = c.state[2 * row], held = c.state[2 * row + 1];
   auto pos_of = [&](int r) {
     const int x = __ldg(p.pos + t0 + (r0 + r) / G);
     return x < len && x >> lb < held ? x : -1;
   };
-  // positions ascend along a request's tokens
-  const int mp = pos_of(rows - 1);
+  int mp = -1;  // largest position of the tile
+  for (int r = lane; r < rows; r += 32) mp = max(mp, pos_of(r));
+  mp = __reduce_max_sync(~0u, mp);
   const int own = mp < 0 ? -1 : mp >> lb;
   const int b0 = min(own + 1, split * split_blocks), b1 = min(own + 1, b0 + split_blocks);
   if (split > 0 && b0 >= b1) return;

@@ -38,6 +38,7 @@ struct Slab {
   int chunk;         // blocks per CTA of kernel one
   int nchunk;
   int stride;        // floats per screen-score row
+  int tiles;         // bound on the tiles of the launch
 };
 
 // Row r's part of the slab.
@@ -88,7 +89,7 @@ score_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, float
     tok0 = clip(__ldg(p.cu + row), sl);
     r0 = (u - tile_base(p, sl, row, G)) * 16;
     nrows = (clip(__ldg(p.cu + row + 1), sl) - tok0) * G;
-    if (r0 >= nrows) return;
+    if (r0 < 0 || r0 >= nrows) return;
   }
   const int rows = min(16, nrows - r0);
   int nb = 0;
@@ -396,7 +397,7 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
   const int tile = sl.per_token ? (tok - sl.t0) * ((G + 15) / 16) + (h % G) / 16
                                 : tile_base(p, sl, row, G) + ((tok - clip(__ldg(p.cu + row), sl)) * G + h % G) / 16;
   for (int i = lane; i * sl.chunk < own; i += 32) {
-    const float x = hmax[((size_t)tile * c.h_kv + head) * sl.nchunk + i];
+    const float x = hmax[((size_t)min(max(tile, 0), sl.tiles - 1) * c.h_kv + head) * sl.nchunk + i];
     hm = x > hm || x != x ? x : hm;  // NaN stays
   }
   for (int off = 16; off; off >>= 1) {
@@ -618,6 +619,7 @@ cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, i
     sl.chunk = chunk_of(c, step, h_q);
     sl.nchunk = (c.max_blocks + sl.chunk - 1) / sl.chunk;
     sl.stride = stride_of(c);
+    sl.tiles = (int)tiles;
     const cudaError_t e = c.d == 64 ? launch_slab<64>(c, p, sl, tiles, q, h_q, topk, score, hmax, sel, status, st)
                                     : launch_slab<128>(c, p, sl, tiles, q, h_q, topk, score, hmax, sel, status, st);
     if (e != cudaSuccess) return e;

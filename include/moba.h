@@ -362,8 +362,8 @@ int moba_cache_reset(const moba_cache* cache, void* stream);
 
 /*
  * Block tables and slot maps.  new_len: int32 [rows], the tokens each row is
- * about to get; -1 gives the row's pages back and empties it (they can be
- * taken from the next call on).
+ * about to get; a negative number gives the row's pages back and empties it
+ * (they can be taken from the next call on).
  *
  * Row r needs max(0, ceil((L + n) / B) - pages held) pages.  They are taken
  * from the ring in row order.  A row is served if all pages needed by rows up

@@ -784,3 +784,35 @@ def test_cached_routing_agrees_with_the_prompt_path(W):
     d = (o.float() - out.float())[same]
     assert d.pow(2).mean().sqrt() < 0.1 * out.float().pow(2).mean().sqrt()
     assert (l - lse)[same].abs().max() < 0.5
+
+
+@gpu
+@pytest.mark.parametrize("cu", [[0, 90], [5, 90], [-7, 90], [90, 3], [200, 400]])
+def test_plans_that_contradict_themselves_stay_in_bounds(cu):
+    """First tokens that cannot be: calls end, nothing behind the buffers is touched (what they compute is not defined)."""
+    r = Run(1, 40, 20, 8, 2, 64, 16, "e4m3", 0, 3, seed=4)
+    plan, want, _ = r.tables([100])
+    r.append(plan, want)
+    plan, want, _ = r.tables([90])
+    assert r.append(plan, want) == 0
+    q = r.rand(90, 8, 64).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    odd = moba.CachePlan(torch.tensor(cu, **i32), plan.token_row, plan.token_pos, plan.slot_map)
+    k, v = (torch.zeros((90, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = r.c.alloc_workspace(90, 8)
+    guard = torch.full((92, 8, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    sel = moba.cache_route(r.c, odd, q, 3, workspace=ws)
+    moba.cache_attention(r.c, odd, q, workspace=ws, out=guard[1:91])
+    moba.cache_attention(r.c, odd, q, sel_idx=sel, workspace=ws, out=guard[1:91])
+    moba.check_status(ws)
+    assert (guard[0] == 3).all() and (guard[91] == 3).all()
+    tail = r.c.tail_k.clone()
+    moba.cache_append(r.c, odd, k, v, workspace=ws)
+    moba.check_status(ws)
+    if cu == [0, 90]:
+        return
+    few = moba.CachePlan(torch.tensor([cu[0], cu[1]], **i32), plan.token_row[:3].contiguous(), plan.token_pos[:3].contiguous(),
+                         plan.slot_map[:3].contiguous())
+    moba.cache_append(r.c, few, k[:3].contiguous(), v[:3].contiguous(), workspace=ws)
+    moba.cache_attention(r.c, few, q[:3].contiguous(), workspace=ws)
+    moba.check_status(ws)
