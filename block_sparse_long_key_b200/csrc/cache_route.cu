@@ -554,11 +554,13 @@ int slab_tokens(const View& c, int T, int h_q) {
   return (int)(n < 1 ? 1 : (n < T ? n : T));
 }
 
-// Blocks per CTA of kernel one: the more, the less a tile's look-ups cost, as long as 8 CTAs per SM remain (64 rows of
-// ragged length up to 2048 blocks: 30 us with 256 blocks, 19 with 1024; one row: 6 and 5 us with 256 and 128).
+// Blocks per CTA of kernel one: the more, the less a tile's look-ups cost, as long as 8 CTAs per SM remain (4 where each
+// warp of a CTA has a tile of its own).  A whole call for 64 rows of ragged length up to 2048 blocks takes 49.4, 40.9,
+// 37.6 and 38.6 us with at most 128, 256, 512 and 1024; a single row's kernel one 6.5 us with 128 and 8.7 with 256.
 int chunk_of(const View& c, int slab, int h_q) {
   int per_token;
-  const long long tiles = tiles_of(c, slab, h_q, &per_token) * c.h_kv / (per_token ? 1 : kScoreThreads / 32);
+  long long tiles = tiles_of(c, slab, h_q, &per_token) * c.h_kv;
+  if (!per_token) tiles /= kScoreThreads / 32;
   int chunk = 128;
   const long long least = (per_token ? 8 : 4) * 148;
   while (chunk < 1024 && tiles * ((c.max_blocks + 2 * chunk - 1) / (2 * chunk)) >= least) chunk *= 2;
