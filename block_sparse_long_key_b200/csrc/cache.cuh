@@ -65,10 +65,35 @@ cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, i
 size_t attn_scratch(const View& c, int T, int h_q);
 cudaError_t launch_attention(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk,
                              bf16* out, float* lse, void* scratch, int32_t* status, cudaStream_t st);
-// Attention over all blocks for steps with many tokens per request (cache_attn_rows.cu); `tiles` bounds the tiles of
-// 128 query rows, split_blocks * B is a multiple of 128.
-cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks,
-                                  int nsplit, bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st);
+// Attention over all blocks for the requests of a step that have at least `limit` query rows per KV head
+// (cache_attn_rows.cu); split_blocks * B is a multiple of 128.
+struct Many {
+  int limit;    // at least 64
+  int per_row;  // a row's tiles of 128 begin at place cu * G / 128 + row (1), or at cu * G / 64 (0)
+  int split_blocks, nsplit;
+};
+cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, const Many& many,
+                                  bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st);
+
+// Query rows per KV head of a request in this step (below 1 if the plan makes no sense).
+__device__ __forceinline__ long long request_rows(const Plan& p, int row, int G) {
+  return ((long long)min(__ldg(p.cu + row + 1), p.T) - __ldg(p.cu + row)) * G;
+}
+
+// The last of rows 0 .. rows - 1 that begins at or before place u (row 0 if none does), by a whole warp: two look-ups one
+// after the other for 1024 rows, where halving takes ten of them.
+template <class F>
+__device__ __forceinline__ int last_row(int rows, long long u, F&& place) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = rows;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const unsigned before = __ballot_sync(~0u, i < n && (i == 0 || place(lo + i) <= u));
+    const int k = (31 - __clz(before)) * step;
+    lo += k, n = min(step, n - k);
+  }
+  return lo;
+}
 
 // Where block j of a row is read from: its page (complete blocks), its tail
 // bank, or nowhere (an entry out of range).

@@ -242,6 +242,15 @@ __device__ __forceinline__ Entry make_entry(const View& c, int page, int j, int 
   return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 128.f) / vs, 0.f};
 }
 
+// How the tiles of attn_kernel are found, and what each does of its row.
+enum : int { kPerToken, kSearch, kSlots };
+struct Few {
+  int mode;
+  int limit;      // query rows per KV head from which a request is left to cache_attn_rows.cu
+  int slot_rows;  // kSlots: rows per request
+  int split_blocks, nsplit;
+};
+
 struct Tile {
   int row;        // request
   int head;       // KV head
@@ -367,8 +376,7 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
 template <int D, int KIND, int NW, int NT, bool SEL>
 __global__ void __launch_bounds__(NW * 32, NW <= 4 ? (D == 128 ? 12 : 16) / NW : 1)
 attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* __restrict__ sel, int topk,
-            int per_token, int split_blocks, int nsplit, bf16* __restrict__ out, float* __restrict__ lse,
-            float* __restrict__ part, int32_t* status) {
+            Few few, bf16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int32_t* status) {
   using Ly = Layout<D>;
   constexpr int TR = 8 * NT;  // rows of a tile
   extern __shared__ __align__(128) unsigned char smem[];
@@ -380,6 +388,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   const int G = h_q / c.h_kv;
   const int lb = 31 - __clz(c.B), lu = lb - 4;  // log2 of the tokens and units of a block
 
+  if constexpr (!SEL) asm volatile("griddepcontrol.launch_dependents;");  // cache_attn_rows.cu: nothing there waits for this
   // ---- the tile
   Tile T;
   int split = 0;
@@ -395,7 +404,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     T.head = blockIdx.y;
     split = blockIdx.z;
     const int u = blockIdx.x;
-    if (per_token) {
+    if (few.mode == kPerToken) {
       const int tiles = (G + TR - 1) / TR;
       T.t0 = u / tiles;
       T.row = __ldg(p.row + T.t0);
@@ -403,19 +412,22 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       T.r0 = (u % tiles) * TR;
       T.nrows = G;
     } else {
-      int lo = 0, hi = c.rows;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((long long)__ldg(p.cu + mid) * G / TR + mid <= u) lo = mid; else hi = mid;
+      if (few.mode == kSlots) {
+        const int slots = few.slot_rows / TR;
+        T.row = u / slots;
+        T.t0 = __ldg(p.cu + T.row);
+        T.r0 = (u % slots) * TR;
+      } else {
+        auto place = [&](int r) { return (long long)__ldg(p.cu + r) * G / TR + r; };
+        T.row = last_row(c.rows, u, place);
+        T.t0 = __ldg(p.cu + T.row);
+        T.r0 = (int)(u - place(T.row)) * TR;
       }
-      T.row = lo;
-      T.t0 = __ldg(p.cu + lo);
-      T.r0 = (int)(u - ((long long)T.t0 * G / TR + lo)) * TR;
-      T.nrows = (min(__ldg(p.cu + lo + 1), p.T) - T.t0) * G;
-      if (T.t0 < 0 || T.r0 < 0 || T.r0 >= T.nrows) return;
+      T.nrows = (int)min(request_rows(p, T.row, G), (long long)few.limit);
+      if (T.t0 < 0 || T.r0 < 0 || T.r0 >= T.nrows || T.nrows == few.limit) return;
     }
   }
-  const int len = c.state[2 * T.row], held = c.state[2 * T.row + 1];
+  const int len = c.state[2 * T.row], held = min(c.state[2 * T.row + 1], c.max_blocks);
   const int rows = min(TR, T.nrows - T.r0);  // real rows of the tile
   // Position of a tile row; -1 for rows that see nothing.
   auto pos_of = [&](int r) {
@@ -438,11 +450,16 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
     mp = max(mp, __shfl_xor_sync(~0u, mp, off));
     min_pos = min(min_pos, __shfl_xor_sync(~0u, min_pos, off));
   }
+  // (behind the look-ups above, which this one then overlaps)
+  if (!SEL && few.mode == kPerToken && few.limit != 0x7fffffff && request_rows(p, T.row, G) >= few.limit) return;
   if (tid < rows && split == 0 && pos_of(tid) != __ldg(p.pos + T.t0 + (T.r0 + tid) / G)) set_status(status, kStatusBadTable);
 
   // ---- queries: bf16 in shared memory, fp16 fragments after scaling by a power of two
   auto item_of = [&](int r) {  // (token, query head) of a tile row
     return (size_t)(T.t0 + (T.r0 + r) / G) * h_q + T.head * G + (T.r0 + r) % G;
+  };
+  auto part_of = [&](int r) {  // where its splits' results go
+    return few.mode == kSlots ? ((size_t)T.row * few.slot_rows + T.r0 + r) * c.h_kv + T.head : item_of(r);
   };
   for (int i = tid; i < TR * (D / 8); i += NW * 32) {
     const int r = i / (D / 8), ck = i % (D / 8);
@@ -455,8 +472,8 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
   int b0 = 0, b1 = own + 1;                                        // blocks of this CTA
   bool my_tail = tail;
   if constexpr (!SEL) {
-    b0 = min(b1, split * split_blocks);
-    const int e = min(b1, b0 + split_blocks);
+    b0 = min(b1, split * few.split_blocks);
+    const int e = min(b1, b0 + few.split_blocks);
     my_tail = tail && e == b1 && b0 < b1;
     b1 = e;
     if (split > 0 && b0 >= b1) return;
@@ -680,14 +697,14 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       for (int x = 0; x < 4; ++x) o[x] += a * b[ch + x];
     }
     const size_t item = item_of(r);
-    if (nsplit == 1) {
+    if (few.nsplit == 1) {
       const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
       uint2 y;
       y.x = pack_bf16(o[0] * inv, o[1] * inv), y.y = pack_bf16(o[2] * inv, o[3] * inv);
       *reinterpret_cast<uint2*>(out + item * D + ch) = y;
       if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
     } else {
-      float* b = part + (item * nsplit + split) * Ly::kORow;
+      float* b = part + (part_of(r) * few.nsplit + split) * Ly::kORow;
       *reinterpret_cast<float4*>(b + ch) = make_float4(o[0], o[1], o[2], o[3]);
       if (ch == 0) b[D] = M, b[D + 1] = l;
     }
@@ -697,19 +714,35 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
 // Joins the splits of a (token, query head): WARPS warps take its splits in turn, four at a time in flight.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(128)
-merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float* __restrict__ part,
-             bf16* __restrict__ out, float* __restrict__ lse) {
+merge_kernel(View c, Plan p, int h_q, Many many, Few few, const float* __restrict__ part_many,
+             const float* __restrict__ part_few, bf16* __restrict__ out, float* __restrict__ lse) {
   constexpr int kORow = Layout<D>::kORow, E = D / 32;
   __shared__ float so[WARPS > 1 ? 4 : 1][D], sm[4], sl[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const size_t item = (size_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
-  if (item >= (size_t)p.T * h_q) return;
-  const int tok = (int)(item / h_q), row = __ldg(p.row + tok), pos = __ldg(p.pos + tok);
+  const unsigned item = blockIdx.x * (4 / WARPS) + warp / WARPS;  // T h_q d is below 2^31
+  if (item >= (unsigned)p.T * h_q) return;
+  const int tok = item / (unsigned)h_q, row = __ldg(p.row + tok), pos = __ldg(p.pos + tok);
   if ((unsigned)row >= (unsigned)c.rows) return;
-  const int lb = 31 - __clz(c.B);
+  const int lb = 31 - __clz(c.B), len = c.state[2 * row], held = min(c.state[2 * row + 1], c.max_blocks);
+  int split_blocks = few.split_blocks, nsplit = few.nsplit;
+  bool known = true;
+  size_t place = item;
+  const float* part = part_few;
+  if (many.limit) {
+    const int G = h_q / c.h_kv, h = item - (unsigned)tok * h_q;
+    if (request_rows(p, row, G) >= many.limit) {
+      split_blocks = many.split_blocks, nsplit = many.nsplit, part = part_many;
+    } else if (few.mode == kSlots) {
+      const long long r = ((long long)tok - __ldg(p.cu + row)) * G + h % G;
+      known = r >= 0 && r < few.slot_rows;
+      place = ((size_t)row * few.slot_rows + (known ? r : 0)) * c.h_kv + h / G;
+    }
+  }
+  if (nsplit == 1) return;
+  const float* b = part + place * nsplit * kORow;
   // splits that wrote: as many as the tile's furthest row needs; a row's own are the first of those
-  const int n = pos < 0 || pos >= c.state[2 * row] || pos >> lb >= c.state[2 * row + 1] ? 0 : (pos >> lb) / split_blocks + 1;
-  const float* b = part + item * nsplit * kORow;
+  const bool sees = known && pos >= 0 && pos < len && pos >> lb < held;
+  const int n = sees ? (pos >> lb) / split_blocks + 1 : 0;
   float M = -CUDART_INF_F, l = 0.f, o[E];
 #pragma unroll
   for (int x = 0; x < E; ++x) o[x] = 0.f;
@@ -744,76 +777,114 @@ merge_kernel(View c, Plan p, int h_q, int split_blocks, int nsplit, const float*
     if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
   } else {
 #pragma unroll
-  for (int x = 0; x < E; ++x) so[warp][lane + 32 * x] = o[x];
-  if (lane == 0) sm[warp] = M, sl[warp] = l;
-  __syncthreads();
-  const int ch = threadIdx.x;
-  if (ch >= D) return;
-  M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  l = 0.f;
-  float y = 0.f;
+    for (int x = 0; x < E; ++x) so[warp][lane + 32 * x] = o[x];
+    if (lane == 0) sm[warp] = M, sl[warp] = l;
+    __syncthreads();
+    const int ch = threadIdx.x;
+    if (ch >= D) return;
+    M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    l = 0.f;
+    float y = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float a = sm[w] == -CUDART_INF_F ? (sl[w] == sl[w] ? 0.f : 1.f) : fast_exp2(sm[w] - M);
-    l += a * sl[w];
-    y += a * so[w][ch];
-  }
-  out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (128.f * l));
-  if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
+    for (int w = 0; w < 4; ++w) {
+      const float a = sm[w] == -CUDART_INF_F ? (sl[w] == sl[w] ? 0.f : 1.f) : fast_exp2(sm[w] - M);
+      l += a * sl[w];
+      y += a * so[w][ch];
+    }
+    out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (128.f * l));
+    if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
 // How a step over all blocks is cut up.
 struct Cut {
-  bool many;       // tiles of 128 rows (cache_attn_rows.cu)
+  bool with_many;  // a request may reach the limit
   bool wide;       // tiles of 16 rows instead of 8
-  bool per_token;  // each token on its own, or a request's tokens together, whichever bound is less
-  long long tiles;
-  int split_blocks, nsplit;
+  long long tiles, many_tiles;
+  Few few;
+  Many many;
+  size_t part_many, part_few;  // floats of splits' results
 };
 
-// Long rows are cut into splits of whole blocks, so that even few or uneven
-// rows fill the GPU: about 16 CTAs per SM counted over rows of full length
-// (tiles of 128 rows: 4), and at least 1024 tokens each (512): a split costs a
-// partial result of D + 4 floats per query row, written and read back.
+// Requests with few query rows per KV head go in tiles of 8 or 16 (attn_kernel), those with many in tiles of 128
+// (cache_attn_rows.cu).  Only the device knows which a request is, so both kernels are launched where a request could
+// reach the limit, and each leaves the other's rows alone.  Measured in tiles of 16 and of 128: d = 128, 48 rows of each
+// of 16 requests over 17K keys 255 and 300 us, 64 rows 326 and 300; d = 64, 80 rows of each of 4 requests 199 and 214
+// us, 96 rows 235 and 203.
+//
+// Long rows are cut into splits of whole blocks, so that even few or uneven rows fill the GPU: about 16 CTAs per SM
+// counted over rows of full length (tiles of 128 rows: 8), and at least 1024 tokens each (512): a split costs a partial
+// result of D + 4 floats per query row, written and read back.  Tiles of 128 with 4, 6 and 8 per SM: 16 requests of 16
+// tokens, 4 heads each, over 4K to 30K keys 276, 283 and 241 us; 13 uneven requests of 4 to 700 tokens 455, 446 and
+// 380; 8 chunks of about 600 tokens 403, 413 and 410.
 Cut cut_of(const View& c, int T, int h_q) {
   const int G = h_q / c.h_kv;
-  const long long a = (long long)T * ((G + 15) / 16), b = (long long)T * G / 16 + c.rows;
-  const long long big = (long long)T * G / 128 + (T < c.rows ? T : c.rows);
-  Cut x;
-  x.per_token = a <= b;
-  x.wide = !x.per_token || G > 8;
-  x.tiles = x.per_token ? a : b;
-  // A tile of 128 rows takes about as long as three of 16 (16 rows of 64 and of 32 query rows each over 13K keys:
-  // 338 and 330 us in tiles of 128, 500 and 250 in tiles of 16).
-  x.many = x.tiles >= 3 * big;
-  if (x.many) x.tiles = (long long)T * G / 128 + c.rows;
-  const long long ctas = (x.many ? big : x.tiles) * c.h_kv;
-  const long long want = ((x.many ? 4 : 16) * 148 + ctas - 1) / ctas;
-  const long long step = x.many && c.B < 128 ? 128 / c.B : 1;  // splits of whole key tiles
-  const long long least = (x.many ? 512 : 1024) / c.B;
-  long long blocks = (c.max_blocks + want - 1) / want;
-  if (blocks < least) blocks = least;
-  // a little more than one wave of CTAs (3 per SM at d = 128, 4 at 64) is worse than one of longer ones
-  const long long slots = (c.d == 128 ? 3 : 4) * 148, total = ctas * ((c.max_blocks + blocks - 1) / blocks);
-  if (!x.many && total > slots && total < 2 * slots && ctas <= slots)
-    blocks = (c.max_blocks + slots / ctas - 1) / (slots / ctas);
-  blocks = (blocks + step - 1) / step * step;
-  x.split_blocks = (int)blocks;
-  x.nsplit = (int)((c.max_blocks + blocks - 1) / blocks);
+  const long long all = (long long)T * G;
+  const int limit = c.d == 128 ? 64 : 96;
+  Cut x = {};
+  x.with_many = all >= limit;
+  // tiles, by what a tile's place says: a token, a place among all tokens, or a place among its request's
+  const long long by[3] = {(long long)T * ((G + 15) / 16), all / 16 + c.rows,
+                           x.with_many ? (long long)c.rows * (limit / 16) : 0x7fffffffffffll};
+  x.few.mode = by[0] <= by[1] && by[0] <= by[2] ? kPerToken : (by[1] <= by[2] ? kSearch : kSlots);
+  x.few.limit = x.with_many ? limit : 0x7fffffff;
+  x.few.slot_rows = limit;
+  x.wide = x.few.mode != kPerToken || G > 8;
+  x.tiles = by[x.few.mode];
+  const int active = T < c.rows ? T : c.rows;
+  {
+    const long long ctas = (x.few.mode == kSlots ? active : x.tiles) * c.h_kv;
+    const long long want = (16 * 148 + ctas - 1) / ctas;
+    const long long least = 1024 / c.B;
+    long long blocks = (c.max_blocks + want - 1) / want;
+    if (blocks < least) blocks = least;
+    // a little more than one wave of CTAs (3 per SM at d = 128, 4 at 64) is worse than one of longer ones (2 rows of
+    // 30000 keys, 8 KV heads: 42.5 us as 16 CTAs per SM would have it, 36.2 in one wave)
+    const long long slots = (c.d == 128 ? 3 : 4) * 148, total = ctas * ((c.max_blocks + blocks - 1) / blocks);
+    if (total > slots && total < 2 * slots && ctas <= slots)
+      blocks = (c.max_blocks + slots / ctas - 1) / (slots / ctas);
+    if (x.few.mode == kSlots) {  // most of these CTAs may find nothing to do: four waves of them are enough
+      long long n = 4 * slots / (x.tiles * c.h_kv);
+      if (n < 1) n = 1;
+      if (blocks < (c.max_blocks + n - 1) / n) blocks = (c.max_blocks + n - 1) / n;
+    }
+    x.few.split_blocks = (int)blocks;
+    x.few.nsplit = (int)((c.max_blocks + blocks - 1) / blocks);
+  }
+  if (x.with_many) {
+    // n >= 64 query rows from `first` on cover at least n / 64 >= ceil(n / 128) multiples of 64: places enough, and few
+    // where few tokens meet many rows
+    const long long most = all / limit;  // requests that can reach the limit
+    const long long ctas = (all / 128 + (most < active ? most : active)) * c.h_kv;
+    long long want = (8 * 148 + ctas - 1) / ctas;
+    const long long step = c.B < 128 ? 128 / c.B : 1;  // splits of whole key tiles
+    x.many.per_row = all / 128 + c.rows <= all / 64;
+    x.many_tiles = x.many.per_row ? all / 128 + c.rows : all / 64;
+    // no more tokens than rows are mostly single ones, with nothing to do here: one wave of CTAs
+    if (T <= c.rows && want > 2 * 148 / (x.many_tiles * c.h_kv)) want = 2 * 148 / (x.many_tiles * c.h_kv);
+    if (want < 1) want = 1;
+    long long blocks = (c.max_blocks + want - 1) / want;
+    if (blocks < 512 / c.B) blocks = 512 / c.B;
+    blocks = (blocks + step - 1) / step * step;
+    x.many.limit = limit;
+    x.many.split_blocks = (int)blocks;
+    x.many.nsplit = (int)((c.max_blocks + blocks - 1) / blocks);
+  }
+  const size_t row = (size_t)c.d + 4;
+  if (x.many.nsplit > 1) x.part_many = (size_t)T * h_q * x.many.nsplit * row;
+  if (x.few.nsplit > 1)
+    x.part_few = (x.few.mode == kSlots ? (size_t)c.rows * limit * c.h_kv : (size_t)T * h_q) * x.few.nsplit * row;
   return x;
 }
 
 template <int D, int KIND, int NW, int NT, bool SEL>
 cudaError_t launch_one(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk, dim3 grid,
-                       int per_token, int split_blocks, int nsplit, bf16* out, float* lse, float* part, int32_t* status,
-                       cudaStream_t st) {
+                       const Few& few, bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
   constexpr int smem = Layout<D>::bytes(NW, NT);
   const cudaError_t e = cudaFuncSetAttribute(attn_kernel<D, KIND, NW, NT, SEL>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_kernel<D, KIND, NW, NT, SEL><<<grid, NW * 32, smem, st>>>(c, p, q, h_q, sel, topk, per_token, split_blocks, nsplit,
-                                                                 out, lse, part, status);
+  attn_kernel<D, KIND, NW, NT, SEL><<<grid, NW * 32, smem, st>>>(c, p, q, h_q, sel, topk, few, out, lse, part, status);
   return cudaGetLastError();
 }
 
@@ -822,30 +893,29 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
                        float* lse, float* part, int32_t* status, cudaStream_t st) {
   if (sel) {
     const dim3 grid(p.T, h_q);
+    const Few one{kPerToken, 0x7fffffff, 0, 0, 1};
     // Two warps a row leave the least to the last wave (1024 rows of 32 blocks of 32: 35 us with four, 31.7 with two,
     // 33.6 with one); few rows take more, so that their blocks are read at once.
     if ((long long)p.T * h_q > 2 * 148)
-      return launch_one<D, KIND, 2, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
-    return launch_one<D, KIND, 8, 1, true>(c, p, q, h_q, sel, topk, grid, 0, 0, 1, out, lse, part, status, st);
+      return launch_one<D, KIND, 2, 1, true>(c, p, q, h_q, sel, topk, grid, one, out, lse, part, status, st);
+    return launch_one<D, KIND, 8, 1, true>(c, p, q, h_q, sel, topk, grid, one, out, lse, part, status, st);
   }
   const Cut x = cut_of(c, p.T, h_q);
-  const dim3 grid((unsigned)x.tiles, c.h_kv, x.nsplit);
-  cudaError_t e;
-  if (x.many)
-    e = launch_attention_rows(c, p, q, h_q, (int)x.tiles, x.split_blocks, x.nsplit, out, lse, part, status, st);
-  else if (x.wide)
-    e = launch_one<D, KIND, 4, 2, false>(c, p, q, h_q, nullptr, 0, grid, x.per_token, x.split_blocks, x.nsplit, out, lse,
-                                         part, status, st);
-  else
-    e = launch_one<D, KIND, 4, 1, false>(c, p, q, h_q, nullptr, 0, grid, x.per_token, x.split_blocks, x.nsplit, out, lse,
-                                         part, status, st);
-  if (e != cudaSuccess || x.nsplit == 1) return e;
+  float* part_few = part + x.part_many;
+  const dim3 grid((unsigned)x.tiles, c.h_kv, x.few.nsplit);
+  cudaError_t e =
+      x.wide ? launch_one<D, KIND, 4, 2, false>(c, p, q, h_q, nullptr, 0, grid, x.few, out, lse, part_few, status, st)
+             : launch_one<D, KIND, 4, 1, false>(c, p, q, h_q, nullptr, 0, grid, x.few, out, lse, part_few, status, st);
+  if (e != cudaSuccess) return e;
+  if (x.with_many) e = launch_attention_rows(c, p, q, h_q, (int)x.many_tiles, x.many, out, lse, part, status, st);
+  if (e != cudaSuccess) return e;
+  if (x.part_many + x.part_few == 0) return cudaSuccess;
   const long long items = (long long)p.T * h_q;
-  // (measured with 38K rows of 2 splits: a warp each 438 us in all, a CTA each 472; 32 rows of 64: 61 and 44)
-  if (x.nsplit <= 8)
-    merge_kernel<D, 1><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
+  // (38K rows of 2 splits: a warp each 438 us in all, a CTA each 472; 32 rows of 64: 48 and 40)
+  if (x.with_many || x.few.nsplit <= 8)
+    merge_kernel<D, 1><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.many, x.few, part, part_few, out, lse);
   else
-    merge_kernel<D, 4><<<(unsigned)items, 128, 0, st>>>(c, p, h_q, x.split_blocks, x.nsplit, part, out, lse);
+    merge_kernel<D, 4><<<(unsigned)items, 128, 0, st>>>(c, p, h_q, x.many, x.few, part, part_few, out, lse);
   return cudaGetLastError();
 }
 
@@ -854,7 +924,7 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
 size_t attn_scratch(const View& c, int T, int h_q) {
   if (T == 0) return 0;
   const Cut x = cut_of(c, T, h_q);
-  return x.nsplit == 1 ? 0 : (size_t)T * h_q * x.nsplit * (c.d + 4) * sizeof(float);
+  return (x.part_many + x.part_few) * sizeof(float);
 }
 
 cudaError_t launch_attention(const View& c, const Plan& p, const bf16* q, int h_q, const int32_t* sel, int topk,

@@ -157,9 +157,15 @@ __device__ __forceinline__ float amax8(uint4 x, float m) {
 }
 
 // ONE: blocks of at least a key tile, so that a tile has one pair of scales.
+// This kernel shares nothing with the one before it (attn_kernel on the requests with few rows) and starts as soon as
+// that one's last CTAs have; what comes after must find both done, so the first CTA ends behind it.
+__device__ __forceinline__ void end_of_cta() {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <int D, int KIND, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
-attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_blocks, int nsplit,
+attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
                  bf16* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int32_t* status) {
   using Ly = Layout<D>;
   extern __shared__ unsigned char smem_raw[];
@@ -174,17 +180,16 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   const int G = h_q / c.h_kv, head = blockIdx.y, split = blockIdx.z, u0 = blockIdx.x;
 
   // ---- the tile's rows
-  int lo = 0, hi = c.rows;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((long long)__ldg(p.cu + mid) * G / kRows + mid <= u0) lo = mid; else hi = mid;
-  }
-  const int row = lo, t0 = __ldg(p.cu + row);
-  const int r0 = (int)(u0 - ((long long)t0 * G / kRows + row)) * kRows;
-  const int nrows = (min(__ldg(p.cu + row + 1), p.T) - t0) * G;
-  if (t0 < 0 || r0 < 0 || r0 >= nrows) return;
-  const int rows = min(kRows, nrows - r0);
-  const int len = c.state[2 * row], held = c.state[2 * row + 1];
+  auto place = [&](int r) {
+    const long long first = (long long)__ldg(p.cu + r) * G;
+    return many.per_row ? first / kRows + r : first / 64;
+  };
+  const int row = last_row(c.rows, u0, place), t0 = __ldg(p.cu + row);
+  const int r0 = (int)(u0 - place(row)) * kRows;
+  const long long nrows = request_rows(p, row, G);
+  if (t0 < 0 || r0 < 0 || r0 >= nrows || nrows < many.limit) return end_of_cta();
+  const int rows = (int)min((long long)kRows, nrows - r0);
+  const int len = c.state[2 * row], held = min(c.state[2 * row + 1], c.max_blocks);
   auto pos_of = [&](int r) {
     const int x = __ldg(p.pos + t0 + (r0 + r) / G);
     return x < len && x >> lb < held ? x : -1;
@@ -193,8 +198,8 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
   for (int r = lane; r < rows; r += 32) mp = max(mp, pos_of(r));
   mp = __reduce_max_sync(~0u, mp);
   const int own = mp < 0 ? -1 : mp >> lb;
-  const int b0 = min(own + 1, split * split_blocks), b1 = min(own + 1, b0 + split_blocks);
-  if (split > 0 && b0 >= b1) return;
+  const int b0 = min(own + 1, split * many.split_blocks), b1 = min(own + 1, b0 + many.split_blocks);
+  if (split > 0 && b0 >= b1) return end_of_cta();
   const int kt0 = b0 * c.B / kKeys;                                  // split_blocks * B is a multiple of kKeys
   const int kend = min(b1 * c.B, mp + 1);                            // first position behind this CTA's keys
   const int nt = mp < 0 ? 0 : (kend - kt0 * kKeys + kKeys - 1) / kKeys;
@@ -526,7 +531,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
           for (int x = 0; x < 16; ++x) o[x] = 0;
         }
         if (tid < rows) {
-          if (nsplit == 1) {
+          if (many.nsplit == 1) {
 #pragma unroll
             for (int x = 0; x < 16; x += 8) {
               uint4 y;
@@ -538,17 +543,17 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
               *reinterpret_cast<uint4*>(out + item * D + h * 16 + x) = y;
             }
           } else {
-            float* b = part + (item * nsplit + split) * (D + 4);
+            float* b = part + (item * many.nsplit + split) * (D + 4);
 #pragma unroll
             for (int x = 0; x < 16; x += 4) *reinterpret_cast<uint4*>(b + h * 16 + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
           }
         }
       }
       if (tid < rows) {
-        if (nsplit == 1) {
+        if (many.nsplit == 1) {
           lse[item] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994531f;
         } else {
-          float* b = part + (item * nsplit + split) * (D + 4);
+          float* b = part + (item * many.nsplit + split) * (D + 4);
           b[D] = m, b[D + 1] = l;
         }
       }
@@ -569,37 +574,46 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, int split_
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, Ly::TMEM_COLS);
   }
+  end_of_cta();
 }
 
 template <int D, int KIND, bool ONE>
-cudaError_t launch_one(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks, int nsplit,
+cudaError_t launch_one(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, const Many& many,
                        bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
   constexpr int smem = Layout<D>::BYTES;
   const cudaError_t e =
       cudaFuncSetAttribute(attn_rows_kernel<D, KIND, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<D, KIND, ONE><<<dim3(tiles, c.h_kv, nsplit), kThreads, smem, st>>>(c, p, q, h_q, split_blocks, nsplit,
-                                                                                      out, lse, part, status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, c.h_kv, many.nsplit);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_rows_kernel<D, KIND, ONE>, c, p, q, h_q, many, out, lse, part, status);
 }
 
 template <int D, int KIND>
-cudaError_t launch(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks, int nsplit,
+cudaError_t launch(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, const Many& many,
                    bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
   return c.B >= kKeys
-             ? launch_one<D, KIND, true>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
-             : launch_one<D, KIND, false>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
+             ? launch_one<D, KIND, true>(c, p, q, h_q, tiles, many, out, lse, part, status, st)
+             : launch_one<D, KIND, false>(c, p, q, h_q, tiles, many, out, lse, part, status, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, int split_blocks,
-                                  int nsplit, bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
+cudaError_t launch_attention_rows(const View& c, const Plan& p, const bf16* q, int h_q, int tiles, const Many& many,
+                                  bf16* out, float* lse, float* part, int32_t* status, cudaStream_t st) {
   if (c.d == 64)
-    return c.kind == 0 ? launch<64, 0>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
-                       : launch<64, 1>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
-  return c.kind == 0 ? launch<128, 0>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st)
-                     : launch<128, 1>(c, p, q, h_q, tiles, split_blocks, nsplit, out, lse, part, status, st);
+    return c.kind == 0 ? launch<64, 0>(c, p, q, h_q, tiles, many, out, lse, part, status, st)
+                       : launch<64, 1>(c, p, q, h_q, tiles, many, out, lse, part, status, st);
+  return c.kind == 0 ? launch<128, 0>(c, p, q, h_q, tiles, many, out, lse, part, status, st)
+                     : launch<128, 1>(c, p, q, h_q, tiles, many, out, lse, part, status, st);
 }
 
 }  // namespace cache

@@ -53,7 +53,7 @@ __device__ __forceinline__ int tile_base(const Plan& p, const Slab& s, int r, in
 __device__ __forceinline__ int own_block(const View& c, int row, int pos) {
   if (pos < 0) return -1;
   const int j = pos >> (31 - __clz(c.B));
-  return pos < c.state[2 * row] && j < c.state[2 * row + 1] ? j : -2;
+  return pos < c.state[2 * row] && j < min(c.state[2 * row + 1], c.max_blocks) ? j : -2;
 }
 
 // SHARE: the CTA's warps take the blocks of one tile in turn; else each has a tile of its own, and neighbours (mostly of

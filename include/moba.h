@@ -352,7 +352,8 @@ typedef struct moba_cache_plan {
 } moba_cache_plan;
 
 /* Bytes of device workspace that any of the calls below needs for a step of
- * total_new tokens and h_q query heads (0: invalid).  As elsewhere it needs
+ * total_new tokens and h_q query heads (0: invalid; a smaller step may need
+ * more, as its rows are cut into more parts).  As elsewhere it needs
  * no initialisation, its first word is the status word, and calls whose work
  * can overlap on the GPU need a workspace each. */
 size_t moba_cache_workspace_size(const moba_cache* cache, int total_new, int h_q);

@@ -266,6 +266,29 @@ def test_chunks_of_many_tokens(hq, h, d, B, kind, n, scale):
         r.step([a, a // 2 + 1])
 
 
+# A request goes to tiles of 128 query rows from 64 (d = 128) or 96 (d = 64) on, another of the same step to small ones.
+MIXED = [
+    # long rows are cut into splits; lists of new tokens around the limit
+    ((8, 2, 128, 64, "e4m3"), [2500, 700, 0, 1300, 64, 1], [[1, 17, 16, 15, 1, 0], [1, 1, 1, 130, 1, 1], [33, 0, 0, 0, 0, 0]]),
+    ((2, 2, 64, 32, "int8"), [2600, 900, 31, 0], [[1, 97, 96, 95], [0, 2, 193, 1], [100, 100, 1, 128]]),
+    ((24, 1, 64, 16, "e4m3"), [1400, 40, 3, 800, 0], [[3, 4, 5, 1, 0], [1, 1, 1, 1, 1], [4, 0, 0, 4, 2]]),
+    ((48, 1, 128, 128, "int8"), [1300, 129, 0], [[1, 1, 1], [2, 1, 0], [0, 3, 9]]),
+    ((4, 1, 128, 32, "e4m3"), [3000], [[15], [16], [50]]),
+    ((1, 1, 128, 16, "int8"), [1100] + [20] * 40, [[1] * 41, [0] * 20 + [64] + [1] * 20, [2] * 40 + [70]]),
+]
+
+
+@gpu
+@pytest.mark.parametrize("shape,held,steps", MIXED, ids=lambda x: str(x) if isinstance(x, tuple) else None)
+def test_steps_of_long_chunks_and_single_tokens(shape, held, steps):
+    hq, h, d, B, kind = shape
+    r = Run(len(held), sum(n // B + 20 for n in held), max(held) // B + 24, hq, h, d, B, kind, 0, 3, seed=B + hq)
+    plan, want, _ = r.tables(held)
+    assert r.append(plan, want) == 0
+    for i, new in enumerate(steps):
+        r.step(new, pad=(0, 3, 40)[i])
+
+
 def _route_alone(cent, q, own_tokens, B, topk, max_blocks=None, T_pad=0):
     """cache_route on centroids given as float64 [blocks, h, d] (split into hi + lo here), one row whose last token is
     the query's; returns sel [1, h_q, topk] and the centroids as held."""
