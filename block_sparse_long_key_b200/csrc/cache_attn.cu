@@ -30,6 +30,14 @@
 // those of tokens 4 t .. 4 t + 3; its share of V is those 4 token rows of D / 8
 // contiguous channels, transposed 4 x 4 bytes in registers, and row r of
 // output tile i is channel (D / 8) (r % 8) + 2 i + r / 8.
+//
+// Each warp has its own ring of pages on their way (cp.async) and its own
+// softmax, joined at the end of the CTA; no warp waits for another.  Bound by
+// HBM: 24 single tokens of 32 heads over 4K to 64K keys of 8 heads of 128
+// (1.17 GB) 220 us, of which the kernel 205 at 5.8 TB/s and the join of the
+// splits 7; 64 rows of 16 heads of 64 over their 32 selected blocks of 32 (134
+// MB) 32 us, 4.4 TB/s, the rest the look-ups before the first page.  One token
+// over 64K keys of 8 heads 39 us, of 32 selected blocks 8.6.
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
@@ -753,8 +761,13 @@ merge_kernel(View c, Plan p, int h_q, Many many, Few few, const float* __restric
       const float* d = b + min(s0 + i, n - 1) * kORow;
       m[i] = s0 + i < n ? d[D] : -CUDART_INF_F;
       ls[i] = s0 + i < n ? d[D + 1] : 0.f;
-#pragma unroll
-      for (int x = 0; x < E; ++x) v[i][x] = d[lane + 32 * x];
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(d + 4 * lane);
+        v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(d + 2 * lane);
+        v[i][0] = y.x, v[i][1] = y.y;
+      }
       top = fmaxf(top, m[i]);
     }
     const float a0 = M == -CUDART_INF_F ? 0.f : fast_exp2(M - top);
@@ -773,11 +786,16 @@ merge_kernel(View c, Plan p, int h_q, Many many, Few few, const float* __restric
   if constexpr (WARPS == 1) {
     const float inv = l == 0.f ? 0.f : 1.f / (128.f * l);
 #pragma unroll
-    for (int x = 0; x < E; ++x) out[item * D + lane + 32 * x] = __float2bfloat16_rn(l == 0.f ? 0.f : o[x] * inv);
+    for (int x = 0; x < E; ++x) o[x] = l == 0.f ? 0.f : o[x] * inv;
+    bf16* y = out + (size_t)item * D + E * lane;
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+    else
+      *reinterpret_cast<uint32_t*>(y) = pack_bf16(o[0], o[1]);
     if (lane == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;
   } else {
 #pragma unroll
-    for (int x = 0; x < E; ++x) so[warp][lane + 32 * x] = o[x];
+    for (int x = 0; x < E; ++x) so[warp][E * lane + x] = o[x];
     if (lane == 0) sm[warp] = M, sl[warp] = l;
     __syncthreads();
     const int ch = threadIdx.x;
@@ -816,7 +834,7 @@ struct Cut {
 // counted over rows of full length (tiles of 128 rows: 8), and at least 1024 tokens each (512): a split costs a partial
 // result of D + 4 floats per query row, written and read back.  Tiles of 128 with 4, 6 and 8 per SM: 16 requests of 16
 // tokens, 4 heads each, over 4K to 30K keys 276, 283 and 241 us; 13 uneven requests of 4 to 700 tokens 455, 446 and
-// 380; 8 chunks of about 600 tokens 403, 413 and 410.
+// 380; 3 chunks of 312 to 513 tokens 403, 413 and 410.
 Cut cut_of(const View& c, int T, int h_q) {
   const int G = h_q / c.h_kv;
   const long long all = (long long)T * G;

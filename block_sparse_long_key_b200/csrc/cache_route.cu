@@ -16,6 +16,11 @@
 // bits and ranked by (score, block).  Products of bf16 are exact in 64 bits
 // and their sums are off by 2^-46 at most, so the result is that of exact
 // arithmetic unless two scores agree to 14 digits.
+//
+// Measured: 64 rows of up to 64K tokens (2048 blocks), 16 heads of 64: 38.6 us, 145 MB of centroids with lo and 73
+// without; kernel one 27 us of it at 2.6 TB/s (uneven rows, short loops behind dependent look-ups), kernel two 17 (a
+// chain of about 40 warp-wide steps per query row), overlapped at the seam.  One row 19 us, nearly all of it that
+// chain.  530 tokens of 32 heads: 30 and 60 us, bound by issue.
 #include <math_constants.h>
 
 #include <climits>
