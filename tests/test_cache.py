@@ -706,6 +706,45 @@ def test_a_generation_step_replays_from_a_graph():
 
 
 @gpu
+@pytest.mark.parametrize("d,hq,h", [(128, 8, 2), (64, 2, 2)])
+def test_a_mixed_step_replays_from_a_graph(d, hq, h):
+    """Attention over all blocks of chunks beside single tokens, captured with what comes before and after it: a replay
+    gives what a call gives, and the calls around it see its inputs and outputs."""
+    r = Run(4, 160, 60, hq, h, d, 64, "e4m3", 0, 3, seed=d)
+    plan, want, _ = r.tables([2000, 900, 130, 5])
+    assert r.append(plan, want) == 0
+    plan, want, _ = r.tables([1, 120, 1, 33], pad=3)
+    assert r.append(plan, want) == 0
+    T = plan.token_row.shape[0]
+    q_in, q, res = (torch.zeros((T, hq, d), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    ws, ws2 = r.c.alloc_workspace(T, hq), r.c.alloc_workspace(T, hq)
+
+    def step():
+        q.copy_(q_in)
+        out, lse = moba.cache_attention(r.c, plan, q, workspace=ws)
+        res.copy_(out)
+        return out, lse
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step()
+    real = want[0][-1]
+    for _ in range(5):
+        q_in.copy_(r.rand(T, hq, d))
+        for _ in range(3):
+            graph.replay()
+        exp, exp_lse = moba.cache_attention(r.c, plan, q_in, workspace=ws2)
+        assert moba.check_status(ws) == 0 and moba.check_status(ws2) == 0
+        assert torch.equal(out[:real], exp[:real]) and torch.equal(lse[:real], exp_lse[:real])
+        assert torch.equal(res[:real], exp[:real])
+
+
+@gpu
 def test_two_streams_with_a_workspace_each():
     """Steps of two caches on two streams at once give what they give alone."""
     a, b = (Run(2, 60, 40, 4, 1, 128, 16, kind, 0, 4, seed=i) for i, kind in enumerate(("e4m3", "int8")))
