@@ -471,25 +471,31 @@ def cache_tables(cache: Cache, new_len: torch.Tensor, total_new: int, row_state_
     (moba_cache_tables).  Advances the cache's row_state and ring, or writes the state after the step to
     ``row_state_out`` / ``ring_out``.  Returns the plan the other calls take (written into ``plan`` if given)."""
     _need_shape(new_len, torch.int32, "new_len", (cache.rows,))
-    T, dev = int(total_new), cache.device
+    T = int(total_new)
     if T < 0:
         raise ValueError("total_new must not be negative")
+    if new_len.get_device() != cache.index:
+        raise ValueError("new_len is on %s, the cache on %s" % (new_len.device, cache.device))
     if row_state_out is not None:
         _need_shape(row_state_out, torch.int32, "row_state_out", (cache.rows, 2))
     if ring_out is not None:
         _need_shape(ring_out, torch.int64, "ring_out", (2,))
     if plan is None:
-        # one allocation, its parts 16-byte aligned
-        a, b = (cache.rows + 4) & ~3, (T + 3) & ~3
-        cu, _, row, _, pos, _, slot, _ = torch.empty(a + 3 * b, dtype=torch.int32, device=dev).split_with_sizes(
-            (cache.rows + 1, a - cache.rows - 1, T, b - T, T, b - T, T, b - T))
+        # one allocation, its parts 16-byte aligned (making a view takes longer than the kernel: no more than needed;
+        # integers have no gradient that the plain split would look after)
+        R, pad = cache.rows + 1, -T & 3
+        buf = new_len.new_empty(3 * (T + pad) + R)
+        if pad:
+            row, _, pos, _, slot, _, cu = buf.unsafe_split_with_sizes((T, pad, T, pad, T, pad, R))
+        else:
+            row, pos, slot, cu = buf.unsafe_split_with_sizes((T, T, T, R))
         plan = CachePlan.__new__(CachePlan)._set(cu, row, pos, slot, T)
     else:
         _check_plan(cache, plan)
         if plan.total_new != T:
             raise ValueError("the plan has room for %d tokens, not total_new = %d" % (plan.total_new, T))
     ws = cache.alloc_workspace(0) if workspace is None else workspace
-    _same_device(cache, new_len=new_len, row_state_out=row_state_out, ring_out=ring_out, workspace=ws)
+    _same_device(cache, row_state_out=row_state_out, ring_out=ring_out, workspace=ws)
     _launch(cache, "moba_cache_tables", new_len.data_ptr(), _addr(row_state_out), _addr(ring_out), plan._ref,
             ws.data_ptr(), ws.numel())
     return plan
