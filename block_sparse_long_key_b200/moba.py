@@ -393,6 +393,8 @@ class Cache:
         self._ref = ctypes.byref(self.struct)
 
     def workspace_size(self, total_new: int, h_q: Optional[int] = None) -> int:
+        """Bytes that a step of total_new tokens needs; a smaller step may need more (its rows are cut finer), so one
+        workspace for many steps takes the largest of theirs."""
         return int(lib().moba_cache_workspace_size(self._ref, int(total_new), int(h_q or self.h_kv)))
 
     def alloc_workspace(self, total_new: int, h_q: Optional[int] = None) -> torch.Tensor:

@@ -274,6 +274,8 @@ MIXED = [
     ((24, 1, 64, 16, "e4m3"), [1400, 40, 3, 800, 0], [[3, 4, 5, 1, 0], [1, 1, 1, 1, 1], [4, 0, 0, 4, 2]]),
     ((48, 1, 128, 128, "int8"), [1300, 129, 0], [[1, 1, 1], [2, 1, 0], [0, 3, 9]]),
     ((4, 1, 128, 32, "e4m3"), [3000], [[15], [16], [50]]),
+    ((128, 1, 128, 64, "e4m3"), [900, 40, 5], [[1, 1, 1], [2, 0, 1], [1, 3, 0]]),     # one token is past the limit
+    ((96, 1, 64, 32, "int8"), [40, 700], [[1, 1], [0, 2], [1, 0]]),
     ((1, 1, 128, 16, "int8"), [1100] + [20] * 40, [[1] * 41, [0] * 20 + [64] + [1] * 20, [2] * 40 + [70]]),
 ]
 
