@@ -34,8 +34,7 @@
 // Each warp has its own ring of pages on their way (cp.async) and its own
 // softmax, joined at the end of the CTA; no warp waits for another.  Bound by
 // HBM: 24 single tokens of 32 heads over 4K to 64K keys of 8 heads of 128
-// (1.17 GB) 220 us, of which the kernel 205 at 5.8 TB/s and the join of the
-// splits 7; 64 rows of 16 heads of 64 over their 32 selected blocks of 32 (134
+// (1.17 GB) 210 us, of which the kernel about 200 at 5.8 TB/s; 64 rows of 16 heads of 64 over their 32 selected blocks of 32 (134
 // MB) 32 us, 4.4 TB/s, the rest the look-ups before the first page.  One token
 // over 64K keys of 8 heads 39 us, of 32 selected blocks 8.6.
 #include <cuda_fp16.h>
@@ -830,9 +829,11 @@ struct Cut {
 // of 16 requests over 17K keys 255 and 300 us, 64 rows 326 and 300; d = 64, 80 rows of each of 4 requests 199 and 214
 // us, 96 rows 235 and 203.
 //
-// Long rows are cut into splits of whole blocks, so that even few or uneven rows fill the GPU: about 16 CTAs per SM
+// Long rows are cut into splits of whole blocks, so that even few or uneven rows fill the GPU: about 24 CTAs per SM
 // counted over rows of full length (tiles of 128 rows: 8), and at least 1024 tokens each (512): a split costs a partial
-// result of D + 4 floats per query row, written and read back.  Tiles of 128 with 4, 6 and 8 per SM: 16 requests of 16
+// result of D + 4 floats per query row, written and read back.  With 8, 16, 24 and 32 per SM: 24 single tokens over 4K
+// to 64K keys 247, 219, 214 and 215 us, 16 over 30K each 171, 177, 184 and 189, 512 tokens beside 63 single ones 603,
+// 606, 559 and 563.  Tiles of 128 with 4, 6 and 8 per SM: 16 requests of 16
 // tokens, 4 heads each, over 4K to 30K keys 276, 283 and 241 us; 13 uneven requests of 4 to 700 tokens 455, 446 and
 // 380; 3 chunks of 312 to 513 tokens 403, 413 and 410.
 Cut cut_of(const View& c, int T, int h_q) {
@@ -852,12 +853,12 @@ Cut cut_of(const View& c, int T, int h_q) {
   const int active = T < c.rows ? T : c.rows;
   {
     const long long ctas = (x.few.mode == kSlots ? active : x.tiles) * c.h_kv;
-    const long long want = (16 * 148 + ctas - 1) / ctas;
+    const long long want = (24 * 148 + ctas - 1) / ctas;
     const long long least = 1024 / c.B;
     long long blocks = (c.max_blocks + want - 1) / want;
     if (blocks < least) blocks = least;
     // a little more than one wave of CTAs (3 per SM at d = 128, 4 at 64) is worse than one of longer ones (2 rows of
-    // 30000 keys, 8 KV heads: 42.5 us as 16 CTAs per SM would have it, 36.2 in one wave)
+    // 30000 keys, 8 KV heads: 42.5 us as 16 CTAs per SM would have it, 35 in one wave)
     const long long slots = (c.d == 128 ? 3 : 4) * 148, total = ctas * ((c.max_blocks + blocks - 1) / blocks);
     if (total > slots && total < 2 * slots && ctas <= slots)
       blocks = (c.max_blocks + slots / ctas - 1) / (slots / ctas);
@@ -929,8 +930,10 @@ cudaError_t launch_all(const View& c, const Plan& p, const bf16* q, int h_q, con
   if (e != cudaSuccess) return e;
   if (x.part_many + x.part_few == 0) return cudaSuccess;
   const long long items = (long long)p.T * h_q;
-  // (38K rows of 2 splits: a warp each 438 us in all, a CTA each 472; 32 rows of 64: 48 and 40)
-  if (x.with_many || x.few.nsplit <= 8)
+  // (38K rows of 2 splits: a warp each 438 us in all, a CTA each 472; 768 rows of up to 13: 214 and 210; 32 rows of 64:
+  // 48 and 40)
+  const int most = x.few.nsplit > x.many.nsplit ? x.few.nsplit : x.many.nsplit;
+  if (most <= 8 || items > 2 * 16 * 148)
     merge_kernel<D, 1><<<(unsigned)((items + 3) / 4), 128, 0, st>>>(c, p, h_q, x.many, x.few, part, part_few, out, lse);
   else
     merge_kernel<D, 4><<<(unsigned)items, 128, 0, st>>>(c, p, h_q, x.many, x.few, part, part_few, out, lse);
