@@ -22,6 +22,7 @@ constexpr int kMaxWidth = 8;
 // Device pointers and sizes of a cache; kernels take it by value.
 struct View {
   int rows, n_pages, max_blocks, h_kv, d, B, kind, conv_width;
+  int raw_kept;  // of a step's raw keys, how many go to the history: conv_width - 1 + set_back (no conv: 0)
   uint8_t* k;
   uint8_t* v;
   float* k_scale;

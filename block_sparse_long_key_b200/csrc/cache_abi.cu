@@ -26,6 +26,7 @@ bool sizes_ok(const moba_cache* c) {
   if (c->block_size != 16 && c->block_size != 32 && c->block_size != 64 && c->block_size != 128) return false;
   if (c->kind != MOBA_CACHE_E4M3 && c->kind != MOBA_CACHE_INT8) return false;
   if (c->conv_width < 0 || c->conv_width > moba::cache::kMaxWidth) return false;
+  if (c->set_back < 0 || c->set_back > moba::cache::kHistRing + 1 - (c->conv_width > 1 ? c->conv_width : 1)) return false;
   if ((long long)c->n_pages * c->block_size >= (1LL << 31)) return false;
   if ((long long)c->max_blocks * c->block_size >= (1LL << 31)) return false;
   if (c->rows > (1 << 24) || c->h_kv > 65535) return false;
@@ -63,6 +64,7 @@ View view_of(const moba_cache* c) {
   View v;
   v.rows = c->rows, v.n_pages = c->n_pages, v.max_blocks = c->max_blocks, v.h_kv = c->h_kv;
   v.d = c->head_dim, v.B = c->block_size, v.kind = c->kind, v.conv_width = c->conv_width;
+  v.raw_kept = c->conv_width > 1 ? c->conv_width - 1 + c->set_back : 0;
   v.k = static_cast<uint8_t*>(c->k), v.v = static_cast<uint8_t*>(c->v);
   v.k_scale = c->k_scale, v.v_scale = c->v_scale;
   v.cent = static_cast<bf16*>(c->cent);

@@ -20,7 +20,9 @@
 // CTA therefore also does the replacing: it takes the second run along where
 // that reads history too (the first run has fewer than W - 1 tokens), then
 // writes the tail tokens of the later block that shares its bank, and the
-// history, behind a barrier.
+// history, behind a barrier.  The history takes more of a step than the next
+// one's taps reach (W - 1): as many more as a length may be set back by, for
+// where part of the step is taken back its tokens are what comes before.
 //
 // Rounding that depends on nothing but the inputs.  k' is the rounding (to
 // fp32, then bf16) of the value summed in 64 bits: it is formed in 32 bits
@@ -361,7 +363,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     }
     if constexpr (CONV) {
       __syncthreads();  // the history has been read
-      const int m = min(R.n, Wm1);
+      const int m = min(R.n, c.raw_kept);
       for (int i = tid / LANES; i < m * c.h_kv; i += GROUPS) {
         const int rel = R.n - m + i / c.h_kv, head = i % c.h_kv;
         *reinterpret_cast<uint4*>(
@@ -554,8 +556,8 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         }
       }
       if constexpr (CONV) {
-        const int m = min(R.n, Wm1), i = tid / LANES;
-        if (i < m) {
+        const int m = min(R.n, c.raw_kept);
+        for (int i = tid / LANES; i < m; i += GROUPS) {
           const int rel = R.n - m + i;
           *reinterpret_cast<uint4*>(
               c.hist + (((size_t)R.row * kHistRing + ((R.pos0 + rel) & (kHistRing - 1))) * c.h_kv + head) * D + ch) =

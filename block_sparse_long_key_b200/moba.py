@@ -38,7 +38,7 @@ class Shape(ctypes.Structure):
 
 class CacheStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n_pages", "max_blocks", "h_kv", "head_dim", "block_size", "kind",
-                                              "conv_width")] + \
+                                              "conv_width", "set_back")] + \
                [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "cent", "tail_k", "tail_v", "hist",
                                                "block_table", "row_state", "free_pages", "ring")]
 
@@ -356,11 +356,16 @@ class Cache:
     ``alloc_cache`` makes an empty one.  Built from tensors of the caller, those
     that a call does not use may be None (bookkeeping alone needs block_table,
     row_state, free_pages and ring).  The tensors are fixed: write into them,
-    do not rebind them."""
+    do not rebind them.
+
+    ``set_back`` (caches with a key conv): how many tokens a row's length may be
+    set back by, as when only part of a step's drafts are accepted; 0 to
+    17 - conv_width."""
 
     def __init__(self, *, rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: int, block_size: int,
                  kind: str = "e4m3", conv_width: int = 0, k=None, v=None, k_scale=None, v_scale=None, cent=None,
-                 tail_k=None, tail_v=None, hist=None, block_table=None, row_state=None, free_pages=None, ring=None):
+                 tail_k=None, tail_v=None, hist=None, block_table=None, row_state=None, free_pages=None, ring=None,
+                 set_back: int = 0):
         if kind not in CACHE_KINDS:
             raise ValueError("kind must be one of %s, got %r" % (sorted(CACHE_KINDS), kind))
         code, dt8 = CACHE_KINDS[kind]
@@ -384,12 +389,14 @@ class Cache:
             raise ValueError("the cache's tensors must be on one CUDA device")
         self.rows, self.n_pages, self.max_blocks, self.h_kv = int(rows), int(n_pages), int(max_blocks), int(h_kv)
         self.head_dim, self.block_size, self.kind, self.conv_width = int(d), int(B), kind, int(conv_width)
+        self.set_back = int(set_back)
         self.device = devs.pop()
         self.index = self.device.index
         for n, x in given.items():
             setattr(self, n, x)
         self.struct = CacheStruct(self.rows, self.n_pages, self.max_blocks, self.h_kv, self.head_dim, self.block_size,
-                                  code, self.conv_width, **{n: x.data_ptr() for n, x in given.items() if x is not None})
+                                  code, self.conv_width, self.set_back,
+                                  **{n: x.data_ptr() for n, x in given.items() if x is not None})
         self._ref = ctypes.byref(self.struct)
 
     def workspace_size(self, total_new: int, h_q: Optional[int] = None) -> int:
@@ -444,13 +451,16 @@ def _check_plan(cache, plan):
 
 
 def alloc_cache(rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: int, block_size: int,
-                kind: str = "e4m3", conv_width: int = 0, device=None) -> Cache:
-    """An empty cache on ``device`` (default: the current CUDA device)."""
+                kind: str = "e4m3", conv_width: int = 0, device=None, set_back: Optional[int] = None) -> Cache:
+    """An empty cache on ``device`` (default: the current CUDA device).  With a key conv, lengths may be set back by
+    ``set_back`` tokens (default: the most there can be, 17 - conv_width)."""
     if kind not in CACHE_KINDS:
         raise ValueError("kind must be one of %s, got %r" % (sorted(CACHE_KINDS), kind))
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
+    if set_back is None:
+        set_back = _CACHE_HIST + 1 - conv_width if conv_width > 1 else 0
     P, H, B, d = n_pages, h_kv, block_size, head_dim
 
     def new(dtype, *shape):
@@ -462,7 +472,7 @@ def alloc_cache(rows: int, n_pages: int, max_blocks: int, h_kv: int, head_dim: i
               v_scale=new(f32, P, H), cent=new(bf, 2, P, H, d), tail_k=new(bf, rows, 2, H, B, d),
               tail_v=new(bf, rows, 2, H, B, d), hist=new(bf, rows, _CACHE_HIST, H, d) if conv_width > 1 else None,
               block_table=new(i32, rows, max_blocks), row_state=new(i32, rows, 2), free_pages=new(i32, P),
-              ring=new(torch.int64, 2))
+              ring=new(torch.int64, 2), set_back=set_back)
     c.reset()
     return c
 

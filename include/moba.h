@@ -294,10 +294,13 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  *  tail_k, tail_v  bf16 [rows, 2, h_kv, B, d]: the tokens of a row's last two
  *                blocks, block j in bank j mod 2.  A partial block is read
  *                from here.  Because both are kept, a row's length may be
- *                set back by up to B tokens (rejected drafts); with a key
- *                conv by at most 17 - conv_width
+ *                set back (rejected drafts: lower the token count of its
+ *                row_state, its pages stay) to B tokens less than the longest
+ *                it has had since the row was empty, however often; with a
+ *                key conv of width 2 or more to set_back tokens less
  *  hist          bf16 [rows, 16, h_kv, d]: the last raw keys, position p at
- *                p mod 16 (NULL allowed when conv_width <= 1)
+ *                p mod 16 (NULL allowed when conv_width <= 1).  Of a step's
+ *                tokens the last conv_width - 1 + set_back go there
  *  block_table   int32 [rows, max_blocks]: the page of each block of a row;
  *                entries from the row's page count on are stale
  *  row_state     int32 [rows, 2]: tokens held, pages held
@@ -325,6 +328,7 @@ typedef struct moba_cache {
   int32_t block_size; /* 16, 32, 64 or 128 */
   int32_t kind;       /* MOBA_CACHE_E4M3 or MOBA_CACHE_INT8 */
   int32_t conv_width; /* 0 (no key conv) .. 8 */
+  int32_t set_back;   /* with a key conv: tokens a row's length may be set back by, 0 .. 17 - conv_width */
   void* k;
   void* v;
   float* k_scale;

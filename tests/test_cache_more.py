@@ -1,0 +1,87 @@
+"""The paged 8-bit cache at the ends of what its calls allow, against the plain 64-bit cache (cache_ref.py): lengths that
+go back, values of extreme size, steps without tokens."""
+import ctypes
+
+import pytest
+import torch
+
+import cache_ref as cr
+from block_sparse_long_key_b200 import moba
+from test_cache import FAKE, L, Run, _plan, _struct  # noqa: F401  (L: the built library)
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------- lengths that go back
+@pytest.mark.parametrize("W,back", [(0, -1), (4, -1), (4, 14), (8, 10), (2, 16), (0, 17)])
+def test_lengths_cannot_go_back_further_than_the_history(L, W, back):  # noqa: F811
+    ref, pr = ctypes.byref(_struct(conv_width=W, hist=FAKE, set_back=back)), ctypes.byref(_plan())
+    assert L.moba_cache_workspace_size(ref, 4, 2) == 0
+    assert L.moba_cache_append(ref, pr, FAKE, FAKE, FAKE, FAKE, 1 << 30, None) == moba.MOBA_EINVAL
+    fits = _struct(conv_width=W, hist=FAKE, set_back=17 - max(W, 1))
+    assert L.moba_cache_workspace_size(ctypes.byref(fits), 4, 2) > 0
+
+
+def _take_back(r, back):
+    """Sets the rows' lengths back by `back` tokens each (their pages stay)."""
+    for i, s in enumerate(back):
+        r.ref.length[i] -= s
+    r.c.row_state[:, 0] -= torch.tensor(back, dtype=torch.int32, device="cuda")
+
+
+def _write(r, new):
+    plan, want, st = r.tables(new)
+    assert st == 0 and r.append(plan, want) == 0
+
+
+@gpu
+@pytest.mark.parametrize("d,B", [(64, 16), (128, 16), (128, 128)])
+@pytest.mark.parametrize("W", [2, 4, 8])
+def test_part_of_a_step_is_taken_back(W, d, B):
+    """Drafts of n tokens of which n - s are accepted, for every s the header allows: the keys that follow are those of a
+    cache that never saw the rejected ones.  Fewer and more drafts than the conv is wide; blocks end inside."""
+    jobs = [(n, s) for n in (2, 3, 4, 5, 9, 16, 17, 40) for s in range(1, min(n - 1, 17 - W, B) + 1)]
+    rows = len(jobs)
+    r = Run(rows, rows * (140 // B + 4), 140 // B + 4, 2, 2, d, B, "e4m3", W, 3, seed=W + d)
+    _write(r, [(5 * i) % (B + 3) + (i % 3 > 0) * 7 for i in range(rows)])
+    _write(r, [n for n, _ in jobs])
+    _take_back(r, [s for _, s in jobs])
+    _write(r, [1] * rows)                                  # (Run.append compares what is held, bit for bit)
+    _write(r, [i % 4 for i in range(rows)])
+    _write(r, [B if i % 2 else 3 for i in range(rows)])
+
+
+@gpu
+@pytest.mark.parametrize("W", [0, 3])
+def test_lengths_go_back_more_than_once(W):
+    """Each time to no less than the longest length so far less what the header allows."""
+    B = 16
+    r = Run(3, 60, 16, 2, 1, 64, B, "int8", W, 3, seed=11)
+    _write(r, [37, 16, 5])
+    longest = list(r.ref.length)
+    for new, back in (((6, 9, 1), (4, 2, 1)), ((1, 1, 1), (3, 5, 2)), ((2, 3, 20), (4, 3, 9)), ((5, 1, 1), (5, 4, 6)),
+                      ((1, 40, 2), (0, 13, 5))):
+        _write(r, new)
+        longest = [max(a, b) for a, b in zip(longest, r.ref.length)]
+        back = [min(s, n - max(m - min(B, 17 - W), 0)) for s, n, m in zip(back, r.ref.length, longest)]
+        _take_back(r, back)
+        _write(r, [1, 2, 1])
+        longest = [max(a, b) for a, b in zip(longest, r.ref.length)]
+
+
+@gpu
+@pytest.mark.parametrize("W,back", [(4, 0), (4, 3), (8, 9), (2, 15)])
+def test_the_history_holds_what_going_back_needs(W, back):
+    """Of a step's raw keys the last W - 1 + set_back, each at its position mod 16; the others stay as they were."""
+    h, d, B, n = 2, 128, 16, (1, 2, 5, 30, 16)
+    c = moba.alloc_cache(len(n), 40, 4, h, d, B, conv_width=W, set_back=back)
+    c.hist.fill_(-9)
+    k = torch.randn((sum(n), h, d), generator=torch.Generator().manual_seed(W)).to(torch.bfloat16)
+    plan = moba.cache_tables(c, torch.tensor(n, dtype=torch.int32, device="cuda"), sum(n))
+    moba.cache_append(c, plan, k.cuda(), k.cuda(), conv_w=torch.zeros((h, d, W), device="cuda"))
+    want, first = torch.full_like(c.hist, -9).cpu(), 0
+    for r, x in enumerate(n):
+        for p in range(max(0, x - (W - 1 + back)), x):
+            want[r, p % 16] = k[first + p]
+        first += x
+    assert torch.equal(c.hist.cpu(), want)
