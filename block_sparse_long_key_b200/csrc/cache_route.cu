@@ -35,6 +35,9 @@ constexpr int kScoreThreads = 128;
 constexpr int kSelWarps = 4;
 constexpr int kCand = 256;       // candidates held per warp (at most 32 x 32)
 constexpr float kNone = -3.4e38f; // below every finite screen score that can win
+// Squares below the normal range of 32 bits lose up to 2^-150 each, 2^-143 in a sum: added to the sums, so that the bound
+// holds for magnitudes whose squares vanish (below 2^-70 all blocks are then candidates, and scored in 64 bits).
+constexpr float kLostSquares = 7.1746481e-43f;  // 2^-140
 constexpr size_t kScratch = (size_t)256 << 20;  // screen scores held at a time
 
 struct Slab {
@@ -411,7 +414,7 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
     hm = x > hm || x != x ? x : hm;
   }
   // |q . hi| and all its partial sums are at most this: up to 2^126 no screen score can be other than finite
-  const float size = sqrtf(sq) * sqrtf(hm);
+  const float size = sqrtf(sq + kLostSquares) * sqrtf(hm + kLostSquares);
   const bool odd = !(size <= 8.5070592e37f);
   const float e2 = 2.f * (size * 4.8828125e-3f + 1e-30f);
   // K-th largest of the subsets' maxima (K < own, so as many subsets hold a block), from below; 64 subsets do for small K

@@ -7,7 +7,7 @@ import torch
 
 import cache_ref as cr
 from block_sparse_long_key_b200 import moba
-from test_cache import FAKE, L, Run, _plan, _struct  # noqa: F401  (L: the built library)
+from test_cache import FAKE, L, Run, _plan, _route_alone, _route_exact, _struct  # noqa: F401  (L: the built library)
 
 gpu = pytest.mark.gpu
 
@@ -85,3 +85,34 @@ def test_the_history_holds_what_going_back_needs(W, back):
             want[r, p % 16] = k[first + p]
         first += x
     assert torch.equal(c.hist.cpu(), want)
+
+
+# ---------------------------------------------------------------------------------------------------------- magnitudes
+@gpu
+@pytest.mark.parametrize("what", ["tiny_cent", "tiny_query", "small_cent", "small_query", "both", "tiny_beside_zero",
+                                  "subnormal_cent", "subnormal_query"])
+def test_routing_of_small_magnitudes(what):
+    """Scores far inside the range of 32 bits whose squares are not: the blocks are still those of the exact scores."""
+    g = torch.Generator().manual_seed(5)
+    nb, h, d, B, T, hq, topk = 1500, 2, 64, 16, 120, 8, 17
+    cent = torch.randn((nb, h, d), generator=g).double()
+    q = torch.randn((T, hq, d), generator=g).to(torch.bfloat16)
+    if what in ("tiny_cent", "tiny_beside_zero"):
+        cent = cent * 1e-24
+    elif what == "tiny_query":
+        q = (q.float() * 1e-24).to(torch.bfloat16)
+    elif what == "small_cent":                                 # squares just below, and just inside, the normal range
+        cent = cent * 2.0 ** -65
+    elif what == "small_query":
+        q = (q.float() * 2.0 ** -65).to(torch.bfloat16)
+    elif what == "both":
+        cent, q = cent * 2.0 ** -70, (q.float() * 2.0 ** 70).to(torch.bfloat16)
+    elif what == "subnormal_cent":
+        cent, q = cent * 1e-39, (q.float() * 1e20).to(torch.bfloat16)
+    elif what == "subnormal_query":
+        cent, q = cent * 1e20, (q.float() * 1e-39).to(torch.bfloat16)
+    if what == "tiny_beside_zero":
+        cent[::3] = 0
+    own = nb - 1
+    sel, held = _route_alone(cent, q, own * B + 5, B, topk)
+    assert torch.equal(sel, _route_exact(held, q, own, topk))
