@@ -28,8 +28,8 @@
 // fp32, then bf16) of the value summed in 64 bits: it is formed in 32 bits
 // first, with a bound E on its error, and again in 64 bits only where a bf16
 // rounding boundary lies within E (about one element in a thousand).  A
-// block's sum is that of its threads' sums (of at most 8 tokens, in 32 bits)
-// in 64 bits, in a fixed order.
+// block's sum is that of its threads' sums (of at most 8 tokens, in 32 bits,
+// an eighth of each so that none overflows) in 64 bits, in a fixed order.
 #include <cuda_fp8.h>
 
 #include "cache.cuh"
@@ -207,7 +207,7 @@ struct Shape {
   static constexpr int STAGE = 2 * NCH * THREADS;   // 16-byte slots of one head's K and V
   static constexpr int RAW = (BLK + kMaxWidth - 1) * LANES;  // slots of a head's raw keys, with the taps before the block
   static constexpr int bytes(bool conv) { return 2 * STAGE * 16 + THREADS * 8 * 4 + (conv ? 2 * RAW * 16 : 0); }
-  static_assert(NCH * GROUPS == BLK, "tile");
+  static_assert(NCH * GROUPS == BLK && NCH <= 8, "tile");
 };
 
 // Where the sum of channel 8 ck + e of a token group is kept: 8 rows of D / 8 values, rotated so that both the threads
@@ -507,14 +507,18 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         mv = fmaxf(mv, __shfl_xor_sync(~0u, mv, off));
       }
       if ((tid & 31) == 0) red[0][tid >> 5] = mk, red[1][tid >> 5] = mv;
-      float s[8];  // of this thread's tokens: exact unless their exponents span more than 2^13
+      // An eighth of the sum of this thread's tokens (8 at most: it stays finite where the sum would not; an eighth of a
+      // bf16 is exact in 32 bits): exact unless their exponents span more than 2^13.
+      float s[8];
       bf16x8_to_f32(x[0], s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] *= 0.125f;
 #pragma unroll
       for (int i = 1; i < NCH; ++i) {
         float f[8];
         bf16x8_to_f32(x[i], f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] += f[e];
+        for (int e = 0; e < 8; ++e) s[e] = fmaf(f[e], 0.125f, s[e]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) gsum[off0 / NCH * D + sum_place<D>(tid % LANES, e)] = s[e];
@@ -531,7 +535,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         double t = 0.0;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) t += (double)gsum[g * D + sum_place<D>(tid >> 3, tid & 7)];
-        const float mean = (float)(t * (1.0 / B));
+        const float mean = (float)(t * (8.0 / B));
         const bf16 hi16 = __float2bfloat16_rn(mean);
         c.cent[at * D + tid] = hi16;
         c.cent[((size_t)c.n_pages * c.h_kv + at) * D + tid] = __float2bfloat16_rn(mean - __bfloat162float(hi16));

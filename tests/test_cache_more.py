@@ -116,3 +116,22 @@ def test_routing_of_small_magnitudes(what):
     own = nb - 1
     sel, held = _route_alone(cent, q, own * B + 5, B, topk)
     assert torch.equal(sel, _route_exact(held, q, own, topk))
+
+
+@gpu
+@pytest.mark.parametrize("d,B", [(64, 16), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_centroids_of_the_largest_keys(kind, d, B):
+    """Means that 32 bits hold, of tokens whose sums they do not; and signs that cancel."""
+    r = Run(1, 8, 6, 2, 2, d, B, kind, 0, 2, seed=d + B)
+    T = 3 * B + 3
+    plan, want, _ = r.tables([T])
+    k = r.rand(T, 2, d)
+    top = torch.finfo(torch.bfloat16).max
+    k[:B] = top
+    k[B:2 * B] = (1e38 * (1 + 0.1 * k[B:2 * B].float().clamp(-1, 1))).to(torch.bfloat16)
+    k[2 * B:3 * B:2], k[2 * B + 1:3 * B:2] = top, -top
+    assert r.append(plan, want, k, r.rand(T, 2, d)) == 0      # (Run.append compares the centroids with the 64-bit means)
+    cent = r.c.cent.float()
+    assert torch.isfinite(cent).all(dim=(2, 3))[:, r.ref.pages[0][:3]].all()
+    assert (cent[0, r.ref.pages[0][0]] == top).all() and (cent[:, r.ref.pages[0][2]] == 0).all()
