@@ -22,7 +22,6 @@ constexpr int kMaxWidth = 8;
 // Device pointers and sizes of a cache; kernels take it by value.
 struct View {
   int rows, n_pages, max_blocks, h_kv, d, B, kind, conv_width;
-  int raw_kept;  // of a step's raw keys, how many go to the history: conv_width - 1 + set_back (no conv: 0)
   uint8_t* k;
   uint8_t* v;
   float* k_scale;
@@ -57,8 +56,9 @@ constexpr int kRowServed = 1, kRowRelease = 2;
 cudaError_t launch_reset(const View& c, cudaStream_t st);
 cudaError_t launch_tables(const View& c, const int32_t* new_len, int32_t* state_out, long long* ring_out,
                           const Plan& p, RowPlan* rp, int32_t* status, cudaStream_t st);
+// raw_kept: of a step's raw keys, how many go to the history (conv_width - 1 + set_back; no conv: 0).
 cudaError_t launch_append(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* conv_w,
-                          int32_t* status, cudaStream_t st);
+                          int raw_kept, int32_t* status, cudaStream_t st);
 // Workspace of the router and of attention beyond the status word, in bytes.
 size_t route_scratch(const View& c, int T, int h_q);
 cudaError_t launch_route(const View& c, const Plan& p, const bf16* q, int h_q, int topk, int32_t* sel, void* scratch,

@@ -64,7 +64,6 @@ View view_of(const moba_cache* c) {
   View v;
   v.rows = c->rows, v.n_pages = c->n_pages, v.max_blocks = c->max_blocks, v.h_kv = c->h_kv;
   v.d = c->head_dim, v.B = c->block_size, v.kind = c->kind, v.conv_width = c->conv_width;
-  v.raw_kept = c->conv_width > 1 ? c->conv_width - 1 + c->set_back : 0;
   v.k = static_cast<uint8_t*>(c->k), v.v = static_cast<uint8_t*>(c->v);
   v.k_scale = c->k_scale, v.v_scale = c->v_scale;
   v.cent = static_cast<bf16*>(c->cent);
@@ -149,7 +148,8 @@ int moba_cache_append(const moba_cache* cache, const moba_cache_plan* plan, cons
   int32_t* status = static_cast<int32_t*>(workspace);
   MOBA_TRY(cudaMemsetAsync(status, 0, 2 * sizeof(int32_t), st));
   MOBA_TRY(moba::cache::launch_append(view_of(cache), plan_of(plan), static_cast<const bf16*>(k),
-                                      static_cast<const bf16*>(v), conv_w, status, st));
+                                      static_cast<const bf16*>(v), conv_w,
+                                      cache->conv_width > 1 ? cache->conv_width - 1 + cache->set_back : 0, status, st));
   return MOBA_OK;
 }
 

@@ -275,7 +275,7 @@ __device__ __forceinline__ float scale_of(float m) {
 template <int KIND, int D, int BLK, bool CONV>
 __global__ void __launch_bounds__(Shape<D, BLK>::THREADS, (CONV || Shape<D, BLK>::NCH > 4 ? 512 : 768) / Shape<D, BLK>::THREADS)
 append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict__ v, const float* __restrict__ w,
-              int per_token, int heads_per_cta, int32_t* status) {
+              int raw_kept, int per_token, int heads_per_cta, int32_t* status) {
   using S = Shape<D, BLK>;
   constexpr int THREADS = S::THREADS, NCH = S::NCH, LANES = S::LANES, GROUPS = S::GROUPS, B = BLK;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -363,7 +363,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
     }
     if constexpr (CONV) {
       __syncthreads();  // the history has been read
-      const int m = min(R.n, c.raw_kept);
+      const int m = min(R.n, raw_kept);
       for (int i = tid / LANES; i < m * c.h_kv; i += GROUPS) {
         const int rel = R.n - m + i / c.h_kv, head = i % c.h_kv;
         *reinterpret_cast<uint4*>(
@@ -560,7 +560,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
         }
       }
       if constexpr (CONV) {
-        const int m = min(R.n, c.raw_kept);
+        const int m = min(R.n, raw_kept);
         for (int i = tid / LANES; i < m; i += GROUPS) {
           const int rel = R.n - m + i;
           *reinterpret_cast<uint4*>(
@@ -574,7 +574,7 @@ append_kernel(View c, Plan p, const bf16* __restrict__ k, const bf16* __restrict
 }
 
 template <int KIND, int D, int BLK>
-cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int32_t* status,
+cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int raw_kept, int32_t* status,
                        cudaStream_t st) {
   using S = Shape<D, BLK>;
   // Runs of a row start at index cu / B + 2 row at the earliest; with few tokens a row every token stands for its run.
@@ -593,36 +593,36 @@ cudaError_t launch_one(const View& c, const Plan& p, const bf16* k, const bf16* 
     if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   S::bytes(true))) != cudaSuccess)
       return e;
-    append_kernel<KIND, D, BLK, true><<<grid, S::THREADS, S::bytes(true), st>>>(c, p, k, v, w, per_token, (int)per, status);
+    append_kernel<KIND, D, BLK, true><<<grid, S::THREADS, S::bytes(true), st>>>(c, p, k, v, w, raw_kept, per_token, (int)per, status);
   } else {
     if ((e = cudaFuncSetAttribute(append_kernel<KIND, D, BLK, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   S::bytes(false))) != cudaSuccess)
       return e;
-    append_kernel<KIND, D, BLK, false><<<grid, S::THREADS, S::bytes(false), st>>>(c, p, k, v, w, per_token, (int)per, status);
+    append_kernel<KIND, D, BLK, false><<<grid, S::THREADS, S::bytes(false), st>>>(c, p, k, v, w, raw_kept, per_token, (int)per, status);
   }
   return cudaGetLastError();
 }
 
 template <int KIND, int D>
-cudaError_t launch_block(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int32_t* status,
+cudaError_t launch_block(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* w, int raw_kept, int32_t* status,
                          cudaStream_t st) {
   switch (c.B) {
-    case 16: return launch_one<KIND, D, 16>(c, p, k, v, w, status, st);
-    case 32: return launch_one<KIND, D, 32>(c, p, k, v, w, status, st);
-    case 64: return launch_one<KIND, D, 64>(c, p, k, v, w, status, st);
-    default: return launch_one<KIND, D, 128>(c, p, k, v, w, status, st);
+    case 16: return launch_one<KIND, D, 16>(c, p, k, v, w, raw_kept, status, st);
+    case 32: return launch_one<KIND, D, 32>(c, p, k, v, w, raw_kept, status, st);
+    case 64: return launch_one<KIND, D, 64>(c, p, k, v, w, raw_kept, status, st);
+    default: return launch_one<KIND, D, 128>(c, p, k, v, w, raw_kept, status, st);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_append(const View& c, const Plan& p, const bf16* k, const bf16* v, const float* conv_w,
-                          int32_t* status, cudaStream_t st) {
+                          int raw_kept, int32_t* status, cudaStream_t st) {
   if (c.d == 64)
-    return c.kind == 0 ? launch_block<0, 64>(c, p, k, v, conv_w, status, st)
-                       : launch_block<1, 64>(c, p, k, v, conv_w, status, st);
-  return c.kind == 0 ? launch_block<0, 128>(c, p, k, v, conv_w, status, st)
-                     : launch_block<1, 128>(c, p, k, v, conv_w, status, st);
+    return c.kind == 0 ? launch_block<0, 64>(c, p, k, v, conv_w, raw_kept, status, st)
+                       : launch_block<1, 64>(c, p, k, v, conv_w, raw_kept, status, st);
+  return c.kind == 0 ? launch_block<0, 128>(c, p, k, v, conv_w, raw_kept, status, st)
+                     : launch_block<1, 128>(c, p, k, v, conv_w, raw_kept, status, st);
 }
 
 }  // namespace cache
