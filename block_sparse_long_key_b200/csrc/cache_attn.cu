@@ -16,7 +16,9 @@
 // brings the row's largest magnitude to [2^8, 2^9): exact down to 2^-22 of
 // it.  Weights are rounded to fp16 (2^-11; those below 2^-21 of the one at the
 // reference are subnormal, with steps of 2^-31 of it); their sum is kept in fp32
-// from the unrounded ones.
+// from the unrounded ones.  Where all of a row's scales are below 2^-100 (values
+// below 2^-91) the steps stay those of a scale of 2^-100: an output is then off
+// by up to 2^-132 times the largest code for each key.
 //
 // A partial block is bf16 (the tail) and is multiplied as bf16, its weights
 // 2^(s_i log2 e - M + 7) as hi + lo; in M it counts with its largest |v| / 448.

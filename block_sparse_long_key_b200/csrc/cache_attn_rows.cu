@@ -6,7 +6,8 @@
 //   producers (4 warps)  8-bit pages -> fp16 K and V tiles in shared memory
 //                        (128-byte swizzle, two of each); the partial block's
 //                        bf16 goes the same way under a power of two that
-//                        keeps every bit
+//                        brings the largest element to 2^14 (all bits of those
+//                        down to 2^-31 of it; smaller ones in steps of 2^-38)
 //   products (1 thread)  S = Q K^T (M = 128, N = 64, K = d) into one of two
 //                        TMEM tiles, O += P V (N = d, K = 64)
 //   softmax (4 warps)    S from TMEM, weights back into its columns as fp16
@@ -504,11 +505,11 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
       if (__any_sync(~0u, odd)) {
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-          const __half2 z = __float2half2_rn(prm[u].z);
+          const float z = prm[u].z;  // as little as 2^-26: not a factor for 16 bits
 #pragma unroll
           for (int x = 0; x < UK / 2; ++x) {
-            __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&s[0][u * UK / 2 + x]), z);
-            s[0][u * UK / 2 + x] = *reinterpret_cast<const uint32_t*>(&y);
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&s[0][u * UK / 2 + x]));
+            s[0][u * UK / 2 + x] = pack_f16(y.x * z, y.y * z);
           }
         }
       }

@@ -135,3 +135,42 @@ def test_centroids_of_the_largest_keys(kind, d, B):
     cent = r.c.cent.float()
     assert torch.isfinite(cent).all(dim=(2, 3))[:, r.ref.pages[0][:3]].all()
     assert (cent[0, r.ref.pages[0][0]] == top).all() and (cent[:, r.ref.pages[0][2]] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,n", [(4, 1), (96, 1), (96, 3)])   # tiles of 8 and of 128 query rows
+@pytest.mark.parametrize("power", [-27, -90, -106, -112, -118])
+def test_values_far_below_one(kind, hq, n, power):
+    """V of every binary size from 1 down to the end of the normal range, one block of 16 keys of it and nothing else to
+    sum.  The block's scale is about 3 2^power / QMAX; scales below 2^-100 take a factor of their own (`rest`)."""
+    B, d = 16, 64
+    r = Run(1, 8, 6, hq, 1, d, B, kind, 0, 2, seed=hq - power)
+    plan, want, _ = r.tables([B])
+    k, v = r.rand(B, 1, d), r.rand(B, 1, d)
+    v = (v.float() * 2.0 ** power).to(torch.bfloat16)
+    assert r.append(plan, want, k, v) == 0
+    plan, want, _ = r.tables([n])
+    none = torch.zeros((n, 1, d), dtype=torch.bfloat16)
+    assert r.append(plan, want, none, none) == 0
+    q = r.rand(n, hq, d)
+    ws = r.c.alloc_workspace(n, hq)
+    out, lse = moba.cache_attention(r.c, plan, q.cuda(), workspace=ws)
+    assert moba.check_status(ws) == 0
+    ref = list(r.ref.attend(want[1], want[2], q))
+    # check_attention's bound for weights below fp16's normal range, 2^-32 sum |v8_i| max(p vs), with vs as the kernels
+    # take it for the reference, at least 2^-100: then n QMAX 2^-100 stands in place of n max|v|, where that is more.
+    # Weights may be rounded to fp16 twice, before and after that factor: 2^-11 of the mass each.  lse is a sum of two
+    # numbers of up to 2^7, rounded to 2^-18 each.
+    ref[4] = torch.maximum(ref[4], torch.full_like(ref[4], (B + n) * cr.QMAX[kind] * 2.0 ** -100))
+    o, l, mass, size, low = ref
+    out, lse = out.cpu(), lse.cpu()
+    delta = (d + 16) * 2.0 ** -24 * size + 2.0 ** -20
+    tol = 2.0 ** -8 * o.abs() + 2.0 ** -133 + (1 + 2.0 ** -7) * mass * (2.0 ** -10 + 2 * torch.expm1(2 * delta))[..., None] + \
+        2.0 ** -32 * low[..., None]
+    err = (out.double() - o).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert ((lse.double() - l).abs() <= 2 * delta + 2.0 ** -17).all()
+    # And it is an answer, not zeros: at 2^-118 the heaviest of 16 weights is about 2^7 2^-25 (the factor is 2^-25.2 for
+    # e4m3), each is off by 2^-24 / sqrt(12) rms, so the outputs by 2^-25.8 sqrt(16) / 2^-18.2 = 0.02 of their rms.
+    assert err.pow(2).mean().sqrt() <= 0.05 * o.pow(2).mean().sqrt()
