@@ -16,6 +16,7 @@ enum : int32_t {
   kStatusNonFinite = 1 << 6   // a NaN or infinity was stored as 0
 };
 
+constexpr float kSmallScale = 9.0949470e-13f;  // 2^-40: see cache_attn.cu
 constexpr int kHistRing = 16;  // raw keys kept per row for the key conv
 constexpr int kMaxWidth = 8;
 

@@ -10,9 +10,11 @@
 // and log2 of the softmax sum is M + log2 l.  The reference M follows the
 // running maximum only when that has grown by more than 8, so in most steps
 // nothing is reduced across lanes or rescaled.  So no block's product has to be
-// scaled on its own, whatever the spread of the scales (vs is taken as at
-// least 2^-100, so that 1 / vs and l stay finite; the rest of a smaller scale
-// is multiplied into w_i).  Queries are fp16 after a power of two per row that
+// scaled on its own (vs is taken as at least 2^-100, so that 1 / vs and l stay
+// finite; the rest of a smaller scale is multiplied into w_i).  Beside blocks of
+// ordinary size the w_i of a scale below 2^-40 (of zeros, mostly) may be 0 in 32
+// bits; what they add to l is formed without vs.  Of larger scales those that one
+// row sees may lie 2^100 apart.  Queries are fp16 after a power of two per row that
 // brings the row's largest magnitude to [2^8, 2^9): exact down to 2^-22 of
 // it.  Weights are rounded to fp16 (2^-11; those below 2^-21 of the one at the
 // reference are subnormal, with steps of 2^-31 of it); their sum is kept in fp32
@@ -53,6 +55,13 @@ constexpr int kPair = 2;         // units per softmax step
 constexpr float kOffset = 7.f;   // exponent of a weight at the reference
 constexpr float kSlack = 8.f;    // growth of a row's maximum that leaves its reference alone
 constexpr int kListCap = 128;    // list entries held in shared memory at a time
+
+// 2^x down to the end of 32 bits (fast_exp2 gives 0 from 2^-126 on).
+__device__ __forceinline__ float exp2_small(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // ---------------------------------------------------------------- fragments
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -216,9 +225,10 @@ struct State {
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, off));
           x = fmaxf(m[n][b], x);
-          a[b] = x > m[n][b] ? fast_exp2(m[n][b] - x) : 1.f;  // m = -inf: 0
+          const float h = x > m[n][b] ? fast_exp2(0.5f * (m[n][b] - x)) : 1.f;  // m = -inf: 0
+          a[b] = h * h;
           m[n][b] = x;
-          l[n][b] *= a[b];
+          l[n][b] = l[n][b] * h * h;  // in halves: l may be as large as a is small
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -241,14 +251,15 @@ struct __align__(16) Entry {
   float ks;
   float lv;      // log2 of the V scale, taken as at least 2^-100
   float rest;    // V scale over that (1 but for smaller scales)
-  float inv;     // 2^-7 over that
+  float inv;     // 2^-7 over lv's; 0 for a scale below 2^-40, whose weights are added to l without it
   float pad;
 };
 
 __device__ __forceinline__ Entry make_entry(const View& c, int page, int j, int head) {
   const size_t at = (size_t)page * c.h_kv + head;
   const float s = __ldg(c.v_scale + at), vs = fmaxf(s, 7.8886090522101181e-31f);
-  return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs, (1.f / 128.f) / vs, 0.f};
+  return Entry{(long long)at * c.B * c.d, j * c.B, __ldg(c.k_scale + at), log2f(vs), s / vs,
+               s < kSmallScale ? 0.f : (1.f / 128.f) / vs, 0.f};
 }
 
 // How the tiles of attn_kernel are found, and what each does of its row.
@@ -343,14 +354,14 @@ __device__ __forceinline__ void tail_unit(const bf16* tk, const bf16* tv, int fi
     }
   }
   st.raise(mx);
-  // weights 2^(s - M + 7): at most 2^(15 - lv), within bf16
+  // weights 2^(s - M + 7): at most 2^(15 - lv), within bf16; from 2^-112 down where lv is largest, so not cut at 2^-126
   uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const float base[2] = {st.base(n, 0), st.base(n, 1)};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      s[n][x] = fast_exp2(s[n][x] - base[x & 1]);
+      s[n][x] = exp2_small(s[n][x] - base[x & 1]);
       st.l[n][x & 1] += s[n][x] * (1.f / 128.f);
     }
 #pragma unroll
@@ -612,6 +623,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
       __syncwarp();
       const unsigned char* src = ring + (i % Ly::kStages) * Ly::kStage;
       float s[kPair][NT][4], mx[NT][2];
+      bool small = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -CUDART_INF_F;
 #pragma unroll
@@ -619,6 +631,7 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
         const int u = (warp + i * NW) * kPair + x;
         unit_scores<D, KIND, NT>(src + x * 2 * kUnit * D, qf, s[x], g, t);
         const Entry e = list[u < units ? u >> lu : 0];
+        small |= e.inv == 0.f;
         const int p0 = u < units && e.at >= 0 ? e.pos + (u & ((1 << lu) - 1)) * kUnit : 0x7fffffff - kUnit;
         const int tok = p0 + 4 * (g >> 1) + (g & 1);
         const bool cut = p0 + kUnit - 1 > min_pos;
@@ -645,6 +658,19 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
         }
       }
       st.raise(mx);
+      if (small) {  // what the weights of small V scales add to l, without the scale
+#pragma unroll
+        for (int x = 0; x < kPair; ++x) {
+          const int u = (warp + i * NW) * kPair + x;
+          const float lv = list[u < units ? u >> lu : 0].lv;
+          if (list[u < units ? u >> lu : 0].inv != 0.f) continue;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              st.l[n][y & 1] += fast_exp2(s[x][n][y] - lv - (st.base(n, y & 1) + kOffset));
+        }
+      }
 #pragma unroll
       for (int x = 0; x < kPair; ++x) {
         const int u = (warp + i * NW) * kPair + x;
@@ -700,8 +726,8 @@ attn_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, const int32_t* 
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float* b = all + w * kStep + r * Ly::kORow;
-      const float a = b[D] == -CUDART_INF_F ? (b[D + 1] == b[D + 1] ? 0.f : 1.f) : fast_exp2(b[D] - M);
-      l += a * b[D + 1];
+      const float h = b[D] == -CUDART_INF_F ? (b[D + 1] == b[D + 1] ? 0.f : 1.f) : fast_exp2(0.5f * (b[D] - M)), a = h * h;
+      l += h * b[D + 1] * h;
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] += a * b[ch + x];
     }
@@ -771,15 +797,15 @@ merge_kernel(View c, Plan p, int h_q, Many many, Few few, const float* __restric
       }
       top = fmaxf(top, m[i]);
     }
-    const float a0 = M == -CUDART_INF_F ? 0.f : fast_exp2(M - top);
-    l *= a0;
+    const float h0 = M == -CUDART_INF_F ? 0.f : fast_exp2(0.5f * (M - top)), a0 = h0 * h0;
+    l = l * h0 * h0;
 #pragma unroll
     for (int x = 0; x < E; ++x) o[x] *= a0;
     M = top;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = m[i] == -CUDART_INF_F ? (ls[i] == ls[i] ? 0.f : 1.f) : fast_exp2(m[i] - top);
-      l += a * ls[i];
+      const float h = m[i] == -CUDART_INF_F ? (ls[i] == ls[i] ? 0.f : 1.f) : fast_exp2(0.5f * (m[i] - top)), a = h * h;
+      l += h * ls[i] * h;
 #pragma unroll
       for (int x = 0; x < E; ++x) o[x] += s0 + i < n ? a * v[i][x] : 0.f;
     }
@@ -806,9 +832,9 @@ merge_kernel(View c, Plan p, int h_q, Many many, Few few, const float* __restric
     float y = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float a = sm[w] == -CUDART_INF_F ? (sl[w] == sl[w] ? 0.f : 1.f) : fast_exp2(sm[w] - M);
-      l += a * sl[w];
-      y += a * so[w][ch];
+      const float h = sm[w] == -CUDART_INF_F ? (sl[w] == sl[w] ? 0.f : 1.f) : fast_exp2(0.5f * (sm[w] - M));
+      l += h * sl[w] * h;
+      y += h * h * so[w][ch];
     }
     out[item * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : y / (128.f * l));
     if (ch == 0) lse[item] = l == 0.f ? -CUDART_INF_F : (M + log2f(l)) * 0.69314718055994531f;

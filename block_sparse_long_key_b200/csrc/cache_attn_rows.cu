@@ -47,7 +47,7 @@ struct Layout {
   static constexpr uint32_t REGION = kKeys * 128;              // 64 keys of 64 fp16
   static constexpr uint32_t TILE = KB * REGION;
   static constexpr uint32_t Q_OFF = 0, K_OFF = KB * Q_REGION, V_OFF = K_OFF + 2 * TILE;
-  static constexpr uint32_t UNIT_OFF = V_OFF + 2 * TILE;       // float4 [2][kUnits]: ks, log2 vs, rest, 2^-7 / vs
+  static constexpr uint32_t UNIT_OFF = V_OFF + 2 * TILE;       // float4 [2][kUnits]: ks, log2 vs, rest, 2^-7 / vs (0: small)
   static constexpr uint32_t RED_OFF = UNIT_OFF + 2 * kUnits * 16;
   static constexpr uint32_t MB_OFF = RED_OFF + 64;             // K full, V full, S full, P full, O done: two each
   static constexpr uint32_t HOLD_OFF = MB_OFF + 80;
@@ -160,6 +160,26 @@ __device__ __forceinline__ float amax8(uint4 x, float m) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
   return m;
+}
+
+// What the weights of a tile's small V scales add to l, without the scale: from the scores once more (UK keys under one
+// pair of scales).  Out of line: it is seldom called, and in place it cost every tile (blocks of 32: 459 to 478 us).
+template <int UK>
+__device__ __noinline__ float small_scales(uint32_t tm_s, const float4* prm, float fac, int nvis, float m) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int x0 = 0; x0 < kKeys; x0 += 16) {
+    const float4 pr = prm[x0 / UK];
+    if (pr.w != 0.f) continue;
+    const float f1 = fmaxf(fac * pr.x, 7.5231639e-37f);
+    uint32_t w[16];
+    tc::tmem_ld16(tm_s + x0, w);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (x0 + x < nvis) sum += fast_exp2(fmaf(__uint_as_float(w[x]), f1, m == -CUDART_INF_F ? 0.f : -m));
+  }
+  return sum;
 }
 
 // ONE: blocks of at least a key tile, so that a tile has one pair of scales.
@@ -368,8 +388,9 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
       if (!__all_sync(~0u, i < 2 || got(mb_o, i - 2))) { *fail = 1; break; }
       if (lane == 0) {
         const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
-        *reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + pw) * 16) =
-            make_float4(ks, now == -1 ? -CUDART_INF_F : log2f(vc), vs / vc, (1.f / 128.f) / vc);  // nothing: weights 0
+        float4* unit = reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + pw) * 16);
+        *unit = make_float4(ks, now == -1 ? -CUDART_INF_F : log2f(vc), 1.f, (1.f / 128.f) / vc);  // nothing: weights 0
+        if (vs < kSmallScale) unit->z = vs / vc * 1.00000012f, unit->w = 0.f;  // never 1, and 1 to 16 bits
       }
       if (now == -2) {
         put_tail(v_tile, c.tail_v, i, pow2f(14 - tail_e[1]));
@@ -445,7 +466,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
       // the units' scales come with the V tile
       if (!__all_sync(~0u, got(mb_v, i))) { *fail = 1; break; }
       constexpr int NU = ONE ? 1 : kUnits, UK = kKeys / NU;  // groups of keys under one pair of scales
-      bool odd, ok = true;  // odd: a V scale below 2^-100
+      bool odd, ok = true;  // odd: a V scale below 2^-40
       // Weights under the reference as it is, and the tile's maximum beside them (the exponentials leave room for it).
       // Where a row's maximum has outgrown its reference, which is seldom, the reference is moved and the tile done again.
       while (true) {
@@ -482,9 +503,9 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
           l += add;
           break;
         }
-        const float a = up ? fast_exp2(m - mx) : 1.f;
+        const float half = up ? fast_exp2(0.5f * (m - mx)) : 1.f, a = half * half;
         if (up) m = mx;
-        l *= a;
+        l = l * half * half;  // l may be as large as a is small
         if (i > 0) {
           ok = __all_sync(~0u, got(mb_o, i - 1));
           if (!ok) break;
@@ -502,7 +523,8 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
         load();
       }
       if (!ok) { *fail = 1; break; }
-      if (__any_sync(~0u, odd)) {
+      if (__any_sync(~0u, odd)) [[unlikely]] {
+        l += small_scales<UK>(tm_s, prm, fac, nvis, m);
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const float z = prm[u].z;  // as little as 2^-26: not a factor for 16 bits

@@ -174,3 +174,39 @@ def test_values_far_below_one(kind, hq, n, power):
     # And it is an answer, not zeros: at 2^-118 the heaviest of 16 weights is about 2^7 2^-25 (the factor is 2^-25.2 for
     # e4m3), each is off by 2^-24 / sqrt(12) rms, so the outputs by 2^-25.8 sqrt(16) / 2^-18.2 = 0.02 of their rms.
     assert err.pow(2).mean().sqrt() <= 0.05 * o.pow(2).mean().sqrt()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,n", [(4, 1), (96, 1), (4, 30)])   # tiles of 8, of 128 and of 16 query rows
+@pytest.mark.parametrize("where", ["first", "last", "every_other", "tail"])
+def test_blocks_of_zeros_beside_large_values(kind, hq, n, where):
+    """A value of zero counts in the softmax's sum like any other, whatever the size of the others: V of 1e13, of 1 and of
+    1e-20, with whole blocks of zeros before, behind and between."""
+    B, d, held = 32, 64, 6 * 32 + 11
+    for size in (1e13, 1.0, 1e-20):
+        r = Run(1, 20, 14, hq, 1, d, B, kind, 0, 8, seed=hq + n)
+        plan, want, _ = r.tables([held])
+        v = (r.rand(held, 1, d).float() * size).to(torch.bfloat16)
+        blk = torch.arange(held) // B
+        v[{"first": blk < 2, "last": (blk == 4) | (blk == 5), "every_other": blk % 2 == 0, "tail": blk == 6}[where]] = 0
+        assert r.append(plan, want, None, v) == 0
+        plan, want, _ = r.tables([n])
+        new = torch.zeros((n, 1, d)) if where == "tail" else r.rand(n, 1, d).float() * size
+        assert r.append(plan, want, None, new.to(torch.bfloat16)) == 0
+        r.queries(plan, want)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,n", [(4, 1), (96, 1)])
+@pytest.mark.parametrize("held", [64, 75, 90])                 # whole blocks, and a partial one of 11 or 26 tokens
+def test_values_near_the_largest(kind, hq, n, held):
+    """V of 1e38, in blocks and in the partial one, and one new token of 1e10 (scales 2^93 apart; the limit is 2^100)."""
+    r = Run(1, 12, 10, hq, 1, 64, 32, kind, 0, 3, seed=held)
+    plan, want, _ = r.tables([held])
+    v = (r.rand(held, 1, 64).float().clamp(-3.3, 3.3) * 1e38).to(torch.bfloat16)
+    assert r.append(plan, want, None, v) == 0
+    plan, want, _ = r.tables([n])
+    assert r.append(plan, want, None, (r.rand(n, 1, 64).float() * 1e10).to(torch.bfloat16)) == 0
+    r.queries(plan, want)
