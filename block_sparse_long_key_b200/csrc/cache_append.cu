@@ -130,14 +130,15 @@ __device__ __forceinline__ uint4 conv8(int W, const float* w, const float* ws, i
     }
   // In units of 2^-24: the sum is off by W size, SiLU (slope at most 1.1) carries that and adds 12 of its own value
   // (exponential, quotient) and 2 |z| of its value for the exponent's argument (|z SiLU(z)| <= size where that counts),
-  // the last sum and the rounding to 32 bits 2 of the result.  1.1 W + 16 with room:
+  // the last sum and the rounding to 32 bits 2 of the result.  1.1 W + 16 with room, and 2^-140 for what the steps lose
+  // below the normal range (2^-150 each):
   const float e1 = 5.9604645e-8f * (1.2f * (float)W + 18.f);
   float y[8];
   uint32_t open = 0;  // channels whose rounding is not settled
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     y[e] = x0[e] + __fdividef(z[e], 1.f + __expf(-z[e]));
-    const float E = fmaf(size[e], e1, 1.1920929e-7f * fabsf(x0[e]));
+    const float E = fmaf(size[e], e1, fmaf(fabsf(x0[e]), 1.1920929e-7f, 7.1746481e-43f));
     const uint32_t both = pack_bf16(y[e] - E, y[e] + E);
     open |= (uint32_t)(__byte_perm(both, 0, 0x1032) != both || !(fabsf(z[e]) < 80.f)) << e;
   }

@@ -210,3 +210,23 @@ def test_values_near_the_largest(kind, hq, n, held):
     plan, want, _ = r.tables([n])
     assert r.append(plan, want, None, (r.rand(n, 1, 64).float() * 1e10).to(torch.bfloat16)) == 0
     r.queries(plan, want)
+
+
+@gpu
+@pytest.mark.parametrize("W", [2, 4])
+@pytest.mark.parametrize("power", [0, -60, -118, -124, -130])
+def test_converted_keys_of_small_magnitudes(W, power):
+    """Keys, and the conv's products, down to the end of the range: still the rounding of the 64-bit value.  With blocks of
+    128 the tail holds all tokens of these rows."""
+    rows, n, h, d, B = 12, 250, 4, 128, 128
+    g = torch.Generator().manual_seed(W - power)
+    k = (torch.randn((rows * n, h, d), generator=g) * 2.0 ** power).to(torch.bfloat16)
+    w = torch.rand((h, d, W), generator=g) - 0.5
+    c = moba.alloc_cache(rows, 2 * rows, 2, h, d, B, conv_width=W)
+    plan = moba.cache_tables(c, torch.full((rows,), n, dtype=torch.int32, device="cuda"), rows * n)
+    moba.cache_append(c, plan, k.cuda(), torch.zeros_like(k).cuda(), conv_w=w.cuda())
+    got = c.tail_k.cpu().permute(0, 1, 3, 2, 4).reshape(rows, 2 * B, h, d)[:, :n]
+    x = torch.cat([torch.zeros((rows, W, h, d), dtype=torch.float64), k.double().reshape(rows, n, h, d)], 1)
+    z = sum(w[:, :, l].double() * x[:, W - l:W - l + n] for l in range(W))
+    want = (x[:, W:] + z / (1 + torch.exp(-z))).float().to(torch.bfloat16)
+    assert torch.equal(got.float(), want.float()), int((got.float() != want.float()).sum())
