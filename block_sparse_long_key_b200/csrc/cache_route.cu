@@ -353,7 +353,10 @@ select_kernel(View c, Plan p, Slab sl, const bf16* __restrict__ q, int h_q, int 
 #pragma unroll
   for (int i = 0; i < D / 64; ++i) qw[i] = __ldg(reinterpret_cast<const uint32_t*>(qr) + lane + 32 * i);
   const int row = __ldg(p.row + tok), pos = __ldg(p.pos + tok);
-  if ((unsigned)row >= (unsigned)c.rows) return;
+  if ((unsigned)row >= (unsigned)c.rows) {
+    cudaGridDependencySynchronize();  // a step of padding only waits, too: what comes after finds score_kernel done
+    return;
+  }
   int32_t* out = sel + item * topk;
   const int own = own_block(c, row, pos);
   cudaGridDependencySynchronize();  // the screen scores are there

@@ -230,3 +230,19 @@ def test_converted_keys_of_small_magnitudes(W, power):
     z = sum(w[:, :, l].double() * x[:, W - l:W - l + n] for l in range(W))
     want = (x[:, W:] + z / (1 + torch.exp(-z))).float().to(torch.bfloat16)
     assert torch.equal(got.float(), want.float()), int((got.float() != want.float()).sum())
+
+
+# --------------------------------------------------------------------------------------------------- steps of nothing
+@gpu
+def test_steps_of_padding_only_between_others():
+    """Every token is padding: nothing is written, and the calls behind keep their status."""
+    r = Run(2, 20, 8, 4, 2, 64, 16, "e4m3", 2, 3, seed=7)
+    r.step([40, 9])
+    for T in (1, 5, 300):
+        plan, want, _ = r.tables([0, 0], pad=T)
+        assert want[1] == [-1] * T
+        assert r.append(plan, want) == 0
+        r.queries(plan, want)
+        plan, want, st = r.tables([200, 0])                        # more than there are blocks for
+        assert st == moba.STATUS_NO_PAGES
+    r.step([1, 1])
