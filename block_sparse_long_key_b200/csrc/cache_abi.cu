@@ -60,6 +60,14 @@ int check_plan(const moba_cache_plan* p) {
   return check_ptrs({p->token_row, p->token_pos, p->slot_map});
 }
 
+// A step without tokens: nothing to do but for the status word, where there is one.
+int no_tokens(void* ws, size_t bytes, void* stream) {
+  if (!ws) return MOBA_OK;
+  const int rc = check_ws(ws, bytes, kAlign);
+  if (rc != MOBA_OK) return rc;
+  return cudaMemsetAsync(ws, 0, 2 * sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOBA_OK : MOBA_ELAUNCH;
+}
+
 View view_of(const moba_cache* c) {
   View v;
   v.rows = c->rows, v.n_pages = c->n_pages, v.max_blocks = c->max_blocks, v.h_kv = c->h_kv;
@@ -140,7 +148,7 @@ int moba_cache_append(const moba_cache* cache, const moba_cache_plan* plan, cons
   if (rc == MOBA_OK) rc = check_store(cache);
   if (rc != MOBA_OK) return rc;
   if ((long long)plan->total_new * cache->h_kv * cache->head_dim >= (1LL << 31)) return MOBA_EINVAL;
-  if (plan->total_new == 0) return MOBA_OK;
+  if (plan->total_new == 0) return no_tokens(workspace, workspace_bytes, stream);
   if ((rc = check_ptrs({k, v})) != MOBA_OK) return rc;
   if (cache->conv_width > 0 && (rc = check_ptrs({conv_w})) != MOBA_OK) return rc;
   if ((rc = check_ws(workspace, workspace_bytes, kAlign)) != MOBA_OK) return rc;
@@ -160,7 +168,7 @@ int moba_cache_route(const moba_cache* cache, const moba_cache_plan* plan, const
   if (rc == MOBA_OK) rc = check_ptrs({cache->cent, cache->block_table, cache->row_state});
   if (rc != MOBA_OK) return rc;
   if (!step_ok(cache, plan->total_new, h_q, topk)) return MOBA_EINVAL;
-  if (plan->total_new == 0) return MOBA_OK;
+  if (plan->total_new == 0) return no_tokens(workspace, workspace_bytes, stream);
   if ((rc = check_ptrs({q, sel_idx})) != MOBA_OK) return rc;
   if ((rc = check_ws(workspace, workspace_bytes, workspace_need(cache, plan->total_new, h_q))) != MOBA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -178,7 +186,7 @@ int moba_cache_attention(const moba_cache* cache, const moba_cache_plan* plan, c
   if (rc == MOBA_OK) rc = check_store(cache);
   if (rc != MOBA_OK) return rc;
   if (!step_ok(cache, plan->total_new, h_q, sel_idx ? topk : 1)) return MOBA_EINVAL;
-  if (plan->total_new == 0) return MOBA_OK;
+  if (plan->total_new == 0) return no_tokens(workspace, workspace_bytes, stream);
   if ((rc = check_ptrs({q, out, lse})) != MOBA_OK) return rc;
   if (sel_idx && (rc = check_ptrs({sel_idx})) != MOBA_OK) return rc;
   if ((rc = check_ws(workspace, workspace_bytes, workspace_need(cache, plan->total_new, h_q))) != MOBA_OK) return rc;

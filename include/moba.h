@@ -281,6 +281,8 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  *   moba_cache_route      picks each new query's blocks from the centroids;
  *   moba_cache_attention  attends to the picked blocks, or to all of them.
  * Nothing is read back to the host, so a step can be captured into a graph.
+ * A step of no tokens (total_new = 0) needs no token arrays, and only
+ * moba_cache_tables a workspace; one that is given has its status cleared.
  *
  * The buffers (device memory of the caller, 16-byte aligned; contents set by
  * moba_cache_reset and the calls above).  Element order is row-major.

@@ -246,3 +246,25 @@ def test_steps_of_padding_only_between_others():
         plan, want, st = r.tables([200, 0])                        # more than there are blocks for
         assert st == moba.STATUS_NO_PAGES
     r.step([1, 1])
+
+
+@gpu
+def test_a_step_without_tokens_leaves_a_clean_status():
+    c = moba.alloc_cache(2, 10, 4, 2, 64, 16)
+    none = moba.cache_tables(c, torch.zeros(2, dtype=torch.int32, device="cuda"), 0)
+    empty = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda ws: moba.cache_append(c, none, empty, empty, workspace=ws),
+                 lambda ws: moba.cache_route(c, none, empty, 2, workspace=ws),
+                 lambda ws: moba.cache_attention(c, none, empty, workspace=ws)):
+        ws = c.alloc_workspace(0, 2)
+        ws.fill_(255)
+        call(ws)
+        assert moba.check_status(ws) == 0
+
+
+def test_a_step_without_tokens_checks_the_workspace_it_is_given(L):  # noqa: F811
+    ref, none = ctypes.byref(_struct()), ctypes.byref(_plan(total_new=0, token_row=None, token_pos=None, slot_map=None))
+    for ws, size, rc in ((FAKE + 128, 1 << 20, moba.MOBA_EALIGN), (FAKE, 128, moba.MOBA_EWORKSPACE), (None, 0, moba.MOBA_OK)):
+        assert L.moba_cache_append(ref, none, None, None, None, ws, size, None) == rc
+        assert L.moba_cache_route(ref, none, None, 2, 4, None, ws, size, None) == rc
+        assert L.moba_cache_attention(ref, none, None, 2, None, 1, None, None, ws, size, None) == rc
