@@ -129,6 +129,7 @@ int moba_cache_tables(const moba_cache* cache, const int32_t* new_len, int32_t* 
   int rc = check_ptrs({cache->block_table, cache->row_state, cache->free_pages, cache->ring, new_len});
   if (rc == MOBA_OK) rc = check_plan(plan);
   if (rc != MOBA_OK) return rc;
+  if ((long long)plan->total_new * cache->h_kv * cache->head_dim >= (1LL << 31)) return MOBA_EINVAL;
   if (!row_state_out) row_state_out = cache->row_state;
   if (!ring_out) ring_out = cache->ring;
   if ((rc = check_ptrs({row_state_out, ring_out})) != MOBA_OK) return rc;

@@ -268,3 +268,8 @@ def test_a_step_without_tokens_checks_the_workspace_it_is_given(L):  # noqa: F81
         assert L.moba_cache_append(ref, none, None, None, None, ws, size, None) == rc
         assert L.moba_cache_route(ref, none, None, 2, 4, None, ws, size, None) == rc
         assert L.moba_cache_attention(ref, none, None, 2, None, 1, None, None, ws, size, None) == rc
+
+
+def test_more_tokens_than_a_step_may_have_are_refused(L):  # noqa: F811
+    ref, big = ctypes.byref(_struct()), _plan(total_new=1 << 24)     # T h_kv d = 2^31
+    assert L.moba_cache_tables(ref, FAKE, None, None, ctypes.byref(big), FAKE, 1 << 40, None) == moba.MOBA_EINVAL
