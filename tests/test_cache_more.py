@@ -232,6 +232,34 @@ def test_converted_keys_of_small_magnitudes(W, power):
     assert torch.equal(got.float(), want.float()), int((got.float() != want.float()).sum())
 
 
+# ------------------------------------------------------------------------------------------- beside the prompt path
+@gpu
+@pytest.mark.parametrize("W", [1, 4])
+def test_cached_keys_beside_those_of_the_prompt_path(W):
+    """moba_forward forms k' in 32 bits, the cache rounds the 64-bit value: they differ by one step of bf16 at most (and
+    what 32-bit sums lose), and seldom.  With blocks of 128 the last two blocks' keys can be read back from the tail."""
+    B, n, h, d = 128, 200, 2, 64
+    g = torch.Generator().manual_seed(W)
+    k, v = (torch.randn((n, h, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.rand((h, d, W), generator=g) - 0.5
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    prompt = moba.forward(k.cuda(), k.cuda(), v.cuda(), cu, B, 2, conv_w=w.cuda())[3].cpu().double()
+    c = moba.alloc_cache(1, 4, 4, h, d, B, conv_width=W)
+    plan = moba.cache_tables(c, torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    moba.cache_append(c, plan, k.cuda(), v.cuda(), conv_w=w.cuda())
+    cached = c.tail_k[0].cpu().double().permute(0, 2, 1, 3).reshape(2 * B, h, d)[:n]
+    x = torch.cat([torch.zeros((W, h, d), dtype=torch.float64), k.double()])
+    taps = [x[W - l:W - l + n] for l in range(W)]
+    z = sum(w[:, :, l].double() * taps[l] for l in range(W))
+    size = sum(w[:, :, l].double().abs() * taps[l].abs() for l in range(W))
+    exact = k.double() + z / (1 + torch.exp(-z))
+    assert torch.equal(cached, exact.float().to(torch.bfloat16).double())
+    # 32 bits: W + 2 roundings of the sum, 2 + |z| of the exponential and a few of the quotient, relative 2^-24 each
+    off = (1.2 * W + 18) * 2.0 ** -24 * size + 2.0 ** -23 * k.double().abs()
+    assert ((prompt - cached).abs() <= 2.0 ** -7 * exact.abs() + off).all()
+    assert (prompt == cached).double().mean() > 0.99
+
+
 # --------------------------------------------------------------------------------------------------- steps of nothing
 @gpu
 def test_steps_of_padding_only_between_others():
