@@ -301,3 +301,101 @@ def test_a_step_without_tokens_checks_the_workspace_it_is_given(L):  # noqa: F81
 def test_more_tokens_than_a_step_may_have_are_refused(L):  # noqa: F811
     ref, big = ctypes.byref(_struct()), _plan(total_new=1 << 24)     # T h_kv d = 2^31
     assert L.moba_cache_tables(ref, FAKE, None, None, ctypes.byref(big), FAKE, 1 << 40, None) == moba.MOBA_EINVAL
+
+
+# ------------------------------------------------------------------------------------- calls that no other test makes
+@gpu
+@pytest.mark.parametrize("W", [2, 4])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_nan_and_infinite_keys_under_the_conv(kind, W):
+    """They reach the keys of the W - 1 tokens behind as well, in the same step and from the history in the next."""
+    r = Run(2, 30, 8, 2, 2, 64, 16, kind, W, 3, seed=W)
+    for new, bad in (([21, 3], ((0, float("nan")), (15, float("inf")), (20, -float("inf")))), ([1, 14], ((1, float("nan")),)),
+                     ([2, 1], ())):
+        plan, want, _ = r.tables(new)
+        T = sum(new)
+        k = r.rand(T, 2, 64)
+        for t, x in bad:
+            k[t, 0, 3], k[t, 1, 60] = x, -x
+        reached = bad or W > 2          # the last bad key is at position 20 of row 0, whose third step begins at 22
+        assert r.append(plan, want, k) == (moba.STATUS_NONFINITE if reached else 0)
+    r.queries(plan, want)
+
+
+@gpu
+def test_a_plan_is_written_again_and_a_planned_state_is_used():
+    """One set of plan tensors for every step, roomier than the steps; the state after a step planned into other tensors
+    and the step then done with those."""
+    r = Run(3, 40, 12, 4, 2, 64, 16, "e4m3", 3, 3, seed=13)
+    c, T = r.c, 40
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = moba.CachePlan(torch.empty(4, **i32), *(torch.empty(T, **i32) for _ in range(3)))
+    state, ring = torch.empty_like(c.row_state), torch.empty_like(c.ring)
+    then = moba.Cache(rows=3, n_pages=40, max_blocks=12, h_kv=2, head_dim=64, block_size=16, conv_width=3, k=c.k, v=c.v,
+                      k_scale=c.k_scale, v_scale=c.v_scale, cent=c.cent, tail_k=c.tail_k, tail_v=c.tail_v, hist=c.hist,
+                      block_table=c.block_table, row_state=state, free_pages=c.free_pages, ring=ring, set_back=14)
+    for new in ([33, 1, 0], [1, 20, 17], [3, -1, 1], [1, 5, 1]):
+        want = r.ref.tables(new, T)
+        ws = c.alloc_workspace(T, 4)
+        assert moba.cache_tables(c, torch.tensor(new, **i32), T, row_state_out=state, ring_out=ring, plan=plan, workspace=ws) is plan
+        assert moba.check_status(ws) == 0
+        for got, exp in zip(plan, want):
+            assert got.tolist() == exp
+        k, v, q = r.rand(T, 2, 64), r.rand(T, 2, 64), r.rand(T, 4, 64)
+        moba.cache_append(then, plan, k.cuda(), v.cuda(), conv_w=r.w.cuda(), workspace=ws)
+        assert moba.check_status(ws) == 0
+        r.ref.append(want[0], want[4], k, v, r.w)
+        r.c = then
+        r.check_store()
+        r.queries(plan, want, q)
+        r.c = c
+        c.row_state.copy_(state), c.ring.copy_(ring)
+
+
+@gpu
+@pytest.mark.parametrize("W,chunk", [(4, 65536), (0, 30000)])
+def test_a_long_prompt(W, chunk):
+    """64K tokens of 16 heads, whole and in chunks: routing against the centroids that are held, attention of some queries
+    against the tokens that are held, both in 64 bits."""
+    n, h, d, B, topk = 65536, 16, 64, 32, 32
+    g = torch.Generator(device="cuda").manual_seed(W)
+    rand = lambda: torch.randn((n, h, d), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    k, v, q = rand(), rand(), rand()
+    w = torch.rand((h, d, W), generator=g, device="cuda") - 0.5 if W else None
+    c = moba.alloc_cache(1, n // B + 3, n // B + 3, h, d, B, conv_width=W)
+    for first in range(0, n, chunk):
+        m = min(chunk, n - first)
+        at = slice(first, first + m)
+        plan = moba.cache_tables(c, torch.tensor([m], dtype=torch.int32, device="cuda"), m)
+        ws = c.alloc_workspace(m, h)
+        moba.cache_append(c, plan, k[at], v[at], conv_w=w, workspace=ws)
+        sel = moba.cache_route(c, plan, q[at], topk, workspace=ws)
+        got = [moba.cache_attention(c, plan, q[at], sel_idx=s, workspace=ws) for s in (sel, None)]
+        assert moba.check_status(ws) == 0
+        done = (first + m) // B
+        pages = c.block_table[0, :done].long()
+        cent = c.cent[0, pages].double() + c.cent[1, pages].double()
+        x8 = [(a.view(torch.uint8)[pages].view(a.dtype).double() * s[pages].double()[:, :, None, None]).transpose(1, 2).reshape(-1, h, d)
+              for a, s in ((c.k, c.k_scale), (c.v, c.v_scale))]
+        left = (first + m) % B
+        keys, vals = (torch.cat([x, t[0, done % 2, :, :left].double().transpose(0, 1)]) for x, t in zip(x8, (c.tail_k, c.tail_v)))
+        for t in sorted({0, 1, m // 3, m // 2 + 17, m - B - 1, m - 1}):
+            p = first + t
+            own = p // B
+            s = torch.einsum("jhd,hd->hj", cent[:own], q[p].double())
+            top = torch.sort(s, dim=-1, descending=True, stable=True).indices[:, :topk - 1].sort(-1).values
+            want = torch.cat([top, torch.full((h, 1), own, device="cuda")], 1)
+            want = torch.nn.functional.pad(want, (0, topk - want.shape[1]), value=-1)
+            assert torch.equal(sel[t].long(), want), (first, t)
+            score = torch.einsum("lhd,hd->hl", keys[:p + 1], q[p].double()) / d ** 0.5
+            size = torch.einsum("lhd,hd->hl", keys[:p + 1].abs(), q[p].double().abs()).amax(-1, keepdim=True) / d ** 0.5
+            block = torch.arange(p + 1, device="cuda") // B
+            for (out, lse), rows in zip(got, (want, None)):
+                z = score
+                if rows is not None:
+                    z = torch.where((rows[:, None] == block[None, :, None]).any(-1), score, -torch.inf)
+                pr = torch.softmax(z, -1)
+                o, mass = (torch.einsum("hl,lhd->hd", pr, y) for y in (vals[:p + 1], vals[:p + 1].abs()))
+                low = (p + 1) * vals[:p + 1].abs().amax((0, 2))[:, None]
+                ref = [x[None].cpu() for x in (o, torch.logsumexp(z, -1), mass, size[:, 0], low[:, 0])]
+                cr.check_attention(out[t:t + 1].cpu(), lse[t:t + 1].cpu(), ref, d, (first, t, rows is None))
