@@ -3,6 +3,8 @@
 // returns the launch status; none allocates or synchronises.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moba {
@@ -16,7 +18,6 @@ enum : int32_t {
   kStatusNonFinite = 1 << 6   // a NaN or infinity was stored as 0
 };
 
-constexpr float kSmallScale = 9.0949470e-13f;  // 2^-40: see cache_attn.cu
 constexpr int kHistRing = 16;  // raw keys kept per row for the key conv
 constexpr int kMaxWidth = 8;
 
@@ -95,6 +96,35 @@ __device__ __forceinline__ int last_row(int rows, long long u, F&& place) {
     lo += k, n = min(step, n - k);
   }
   return lo;
+}
+
+// ---- what both attention kernels share (the arithmetic: cache_attn.cu)
+constexpr float kOffset = 7.f;                 // exponent of a weight at the reference
+constexpr float kSlack = 8.f;                  // growth of a row's maximum that leaves its reference alone
+constexpr float kSmallScale = 9.0949470e-13f;  // 2^-40: V scales below add to the sum of weights by themselves
+
+// Four 8-bit codes to two fp16 pairs, exactly.
+template <int KIND>
+__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  if constexpr (KIND == 0) {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+  } else {
+    // 0x64bb is 1024 + bb; with bb = x + 128 subtract 1152.
+    x ^= 0x80808080u;
+    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&ra);
+    hi = *reinterpret_cast<const uint32_t*>(&rb);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Where block j of a row is read from: its page (complete blocks), its tail

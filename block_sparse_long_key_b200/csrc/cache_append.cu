@@ -10,8 +10,8 @@
 // consecutive tokens of the block in registers, so a complete block is read
 // once (its earlier tokens from the tail), its largest magnitudes agreed on,
 // and its codes written once.  Bound by HBM for prompts (four of 8K to 64K
-// tokens, 8 heads of 128: 764 MB in 140 us, 5.5 TB/s, 84 % of a copy's rate),
-// by instruction issue with the conv (64K tokens, 16 heads of 64, width 4: 276
+// tokens, 8 heads of 128: 764 MB in 141 us, 5.4 TB/s, 83 % of a copy's rate),
+// by instruction issue with the conv (64K tokens, 16 heads of 64, width 4: 275
 // us, without conv 87), by a chain of look-ups for single tokens (64 rows with
 // conv 10.7 us).
 //

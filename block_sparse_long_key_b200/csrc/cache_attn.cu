@@ -38,10 +38,9 @@
 // Each warp has its own ring of pages on their way (cp.async) and its own
 // softmax, joined at the end of the CTA; no warp waits for another.  Bound by
 // HBM: 24 single tokens of 32 heads over 4K to 64K keys of 8 heads of 128
-// (1.17 GB) 210 us, of which the kernel about 200 at 5.8 TB/s; 64 rows of 16 heads of 64 over their 32 selected blocks of 32 (134
-// MB) 32 us, 4.4 TB/s, the rest the look-ups before the first page.  One token
-// over 64K keys of 8 heads 39 us, of 32 selected blocks 8.6.
-#include <cuda_fp16.h>
+// (1.17 GB) 212 us, of which the kernel about 205 at 5.7 TB/s; 64 rows of 16 heads of 64 over their 32 selected blocks of 32 (134
+// MB) 33 us, 4.3 TB/s, the rest the look-ups before the first page.  One token
+// over 64K keys of 8 heads 39 us, of 32 selected blocks 10.
 #include <math_constants.h>
 
 #include "cache.cuh"
@@ -52,8 +51,6 @@ namespace {
 
 constexpr int kUnit = 16;        // tokens per unit
 constexpr int kPair = 2;         // units per softmax step
-constexpr float kOffset = 7.f;   // exponent of a weight at the reference
-constexpr float kSlack = 8.f;    // growth of a row's maximum that leaves its reference alone
 constexpr int kListCap = 128;    // list entries held in shared memory at a time
 
 // 2^x down to the end of 32 bits (fast_exp2 gives 0 from 2^-126 on).
@@ -70,30 +67,6 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       "{%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Four 8-bit codes to two fp16 pairs, exactly.
-template <int KIND>
-__device__ __forceinline__ void widen(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KIND == 0) {
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-  } else {
-    // 0x64bb is 1024 + bb; with bb = x + 128 subtract 1152.
-    x ^= 0x80808080u;
-    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&ra);
-    hi = *reinterpret_cast<const uint32_t*>(&rb);
-  }
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // 4 x 4 byte transpose: x[i] = row i, y[c] = column c.

@@ -17,12 +17,11 @@
 // of a row moves only when its maximum grows by more than 2^8, so O (in TMEM)
 // is seldom rescaled: weights are 2^(x - m + 7) <= 2^15.
 //
-// Measured on 3 chunks of 312 to 513 tokens, 32 heads of 128 over 8 KV heads (251 GFLOP): 410 us with the join, 0.61
+// Measured on 3 chunks of 312 to 513 tokens, 32 heads of 128 over 8 KV heads (251 GFLOP): 406 us with the join, 0.62
 // PFLOP/s, the tensor pipe busy 32 % of the time.  What bounds it is the softmax warps' chain per tile (load from TMEM,
 // maximum, exponentials, store) and the widening of the codes, which share the issue slots (53 % taken).  Two score
 // tiles and a warp for the products took it from 475 to 461 us, one pair of scales per tile to 438, exponentials under
 // the reference as it is to 396 (with fewer splits).  Eight softmax warps took 454 us where four took 437.
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
@@ -37,8 +36,6 @@ constexpr int kRows = 128;      // query rows per CTA
 constexpr int kKeys = 64;       // key positions per tile
 constexpr int kUnits = 4;       // units of 16 positions per tile, one per producer warp
 constexpr int kThreads = 288;   // 4 softmax warps, 4 producer warps, 1 warp for the products
-constexpr float kOffset = 7.f;
-constexpr float kSlack = 8.f;   // growth of a row's maximum that leaves its reference alone
 
 template <int D>
 struct Layout {
@@ -61,31 +58,13 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Four codes to two fp16 pairs, exactly.
-template <int KIND>
-__device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KIND == 0) {
-    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(x));
-  } else {
-    x ^= 0x80808080u;  // 0x64bb is 1024 + bb; with bb = x + 128 subtract 1152
-    const uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
-    const __half2 off = __half2half2(__ushort_as_half(0x6480));
-    const __half2 ra = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 rb = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&ra);
-    hi = *reinterpret_cast<const uint32_t*>(&rb);
-  }
-}
-
 // 16 codes to 32 bytes of fp16.
 template <int KIND>
 __device__ __forceinline__ void widen16(uint4 w, uint4& a, uint4& b) {
-  widen4<KIND>(w.x, a.x, a.y);
-  widen4<KIND>(w.y, a.z, a.w);
-  widen4<KIND>(w.z, b.x, b.y);
-  widen4<KIND>(w.w, b.z, b.w);
+  widen<KIND>(w.x, a.x, a.y);
+  widen<KIND>(w.y, a.z, a.w);
+  widen<KIND>(w.z, b.x, b.y);
+  widen<KIND>(w.w, b.z, b.w);
 }
 
 // Bounded wait for phase `parity`: the clock is looked at once in 1024 tries.
@@ -137,11 +116,6 @@ __device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // Exponent of a magnitude, within what keeps 2^(14 - e) and 2^(e - 14) normal.
 __device__ __forceinline__ int exponent(float m) { return max(-100, min(127, (int)((__float_as_uint(m) >> 23) & 255) - 127)); }
@@ -182,13 +156,13 @@ __device__ __noinline__ float small_scales(uint32_t tm_s, const float4* prm, flo
   return sum;
 }
 
-// ONE: blocks of at least a key tile, so that a tile has one pair of scales.
 // This kernel shares nothing with the one before it (attn_kernel on the requests with few rows) and starts as soon as
 // that one's last CTAs have; what comes after must find both done, so the first CTA ends behind it.
 __device__ __forceinline__ void end_of_cta() {
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ONE: blocks of at least a key tile, so that a tile has one pair of scales.
 template <int D, int KIND, bool ONE>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
