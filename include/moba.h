@@ -284,6 +284,12 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  * A step of no tokens (total_new = 0) needs no token arrays, and only
  * moba_cache_tables a workspace; one that is given has its status cleared.
  *
+ * A loop: with lengths in new_len, moba_cache_tables(c, new_len, NULL, NULL,
+ * plan, ...), moba_cache_append(c, plan, k, v, conv_w, ...), moba_cache_route(c,
+ * plan, q, h_q, topk, sel, ...), moba_cache_attention(c, plan, q, h_q, sel, topk,
+ * out, lse, ...); then, where drafts were rejected, their number is taken off
+ * the token counts in row_state.
+ *
  * The buffers (device memory of the caller, 16-byte aligned; contents set by
  * moba_cache_reset and the calls above).  Element order is row-major.
  *  k, v          8 bits [n_pages, h_kv, B, d]: complete blocks.  kind 0: e4m3,
@@ -311,7 +317,10 @@ int moba_key_conv_backward(const void* k, const float* conv_w, int conv_width, c
  *
  * h_q (at most 65535), head_dim, block_size, topk and conv_width have the
  * limits of the other calls; max_blocks * B, n_pages * B and T * h_q * max(d, topk) are < 2^31.
- * Offsets into the pages are 64 bits wide.
+ * Offsets into the pages are 64 bits wide.  max_blocks should be no larger than
+ * the longest request needs: the host divides the work of attention and routing
+ * by it, so the same requests take longer under a table many times as wide as
+ * they are long, and need more workspace.
  */
 #define MOBA_CACHE_E4M3 0
 #define MOBA_CACHE_INT8 1
