@@ -364,7 +364,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
         const float vc = fmaxf(vs, 7.8886090522101181e-31f);  // 2^-100
         float4* unit = reinterpret_cast<float4*>(sm + Ly::UNIT_OFF + ((i & 1) * kUnits + pw) * 16);
         *unit = make_float4(ks, now == -1 ? -CUDART_INF_F : log2f(vc), 1.f, (1.f / 128.f) / vc);  // nothing: weights 0
-        if (vs < kSmallScale) unit->z = vs / vc * 1.00000012f, unit->w = 0.f;  // never 1, and 1 to 16 bits
+        if (vs < kSmallScale) unit->z = vs / vc * 0.99999994f, unit->w = 0.f;  // below 1, and the same to 16 bits
       }
       if (now == -2) {
         put_tail(v_tile, c.tail_v, i, pow2f(14 - tail_e[1]));

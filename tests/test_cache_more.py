@@ -232,6 +232,32 @@ def test_converted_keys_of_small_magnitudes(W, power):
     assert torch.equal(got.float(), want.float()), int((got.float() != want.float()).sum())
 
 
+@gpu
+@pytest.mark.parametrize("hq,n", [(4, 1), (96, 1), (4, 30)])
+def test_lse_does_not_depend_on_the_values(hq, n):
+    """V scales on either side of where the kernels take another path, and of their ends, set in the cache by hand."""
+    B, d, held = 16, 64, 5 * 16 + 3
+    r = Run(1, 12, 9, hq, 1, d, B, "int8", 0, 4, seed=n)
+    plan, want, _ = r.tables([held])
+    assert r.append(plan, want) == 0
+    plan, want, _ = r.tables([n])
+    assert r.append(plan, want) == 0
+    q = r.rand(n, hq, d)
+    o, lse_ref, mass, size, low = r.ref.attend(want[1], want[2], q)
+    delta = (d + 16) * 2.0 ** -24 * size + 2.0 ** -20
+    for edge in (2.0 ** -126, 2.0 ** -100, 2.0 ** -40, 1.0, 2.0 ** 40):
+        x = torch.tensor(edge)
+        for scale in (torch.nextafter(x, torch.tensor(0.0)), x, torch.nextafter(x, torch.tensor(1e30))):
+            for pages in (r.ref.pages[0], r.ref.pages[0][1:3]):            # all blocks, and two among ordinary ones
+                r.c.v_scale.fill_(1.0)
+                r.c.v_scale[pages] = scale.item()
+                ws = r.c.alloc_workspace(n, hq)
+                out, lse = moba.cache_attention(r.c, plan, q.cuda(), workspace=ws)
+                assert moba.check_status(ws) == 0
+                # M and log2 l are rounded to 2^-18 each where they are as large as 2^7
+                assert ((lse.cpu().double() - lse_ref).abs() <= 2 * delta + 2.0 ** -17).all(), (edge, scale.item(), len(pages))
+
+
 # ------------------------------------------------------------------------------------------- beside the prompt path
 @gpu
 @pytest.mark.parametrize("W", [1, 4])
