@@ -5,9 +5,12 @@
 // head; row = TMEM lane = softmax thread) and walks key tiles of 64 positions.
 //   producers (4 warps)  8-bit pages -> fp16 K and V tiles in shared memory
 //                        (128-byte swizzle, two of each); the partial block's
-//                        bf16 goes the same way under a power of two that
-//                        brings the largest element to 2^14 (all bits of those
-//                        down to 2^-31 of it; smaller ones in steps of 2^-38)
+//                        bf16 goes the same way under powers of two that bring
+//                        the largest key to 2^14 (all bits of elements down to
+//                        2^-31 of it, smaller ones in steps of 2^-38) and the
+//                        largest value to 2^7, as large as codes are, so that
+//                        what weights lose counts as much beside both (values
+//                        keep all bits down to 2^-24 of it, then steps of 2^-31)
 //   products (1 thread)  S = Q K^T (M = 128, N = 64, K = d) into one of two
 //                        TMEM tiles, O += P V (N = d, K = 64)
 //   softmax (4 warps)    S from TMEM, weights back into its columns as fp16
@@ -35,6 +38,8 @@ namespace {
 constexpr int kRows = 128;      // query rows per CTA
 constexpr int kKeys = 64;       // key positions per tile
 constexpr int kUnits = 4;       // units of 16 positions per tile, one per producer warp
+constexpr int kTailK = 14;      // exponents that the largest key and value of a partial block are brought to: a key's
+constexpr int kTailV = 7;       // smallest bits count, a value is to be as large as an 8-bit code beside the same scale
 constexpr int kThreads = 288;   // 4 softmax warps, 4 producer warps, 1 warp for the products
 
 template <int D>
@@ -339,7 +344,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
       // K tile free: the scores of tile i - 2 are done
       if (!__all_sync(~0u, i < 2 || got(mb_s, i - 2))) { *fail = 1; break; }
       if (pg == -2) {
-        put_tail(k_tile, c.tail_k, i, pow2f(14 - tail_e[0]));
+        put_tail(k_tile, c.tail_k, i, pow2f(kTailK - tail_e[0]));
       } else {
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
@@ -351,8 +356,8 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
       tc::fence_proxy_async();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(mb_k + 8 * (i & 1));
-      const float ks = pg >= 0 ? sc[0] : (pg == -2 ? pow2f(tail_e[0] - 14) : 0.f);
-      const float vs = pg >= 0 ? sc[1] : (pg == -2 ? pow2f(tail_e[1] - 14) : 1.f);
+      const float ks = pg >= 0 ? sc[0] : (pg == -2 ? pow2f(tail_e[0] - kTailK) : 0.f);
+      const float vs = pg >= 0 ? sc[1] : (pg == -2 ? pow2f(tail_e[1] - kTailV) : 1.f);
       const int now = pg;
       pg = unit_page(next, i + 1);
       next = unit_entry(i + 2);
@@ -367,7 +372,7 @@ attn_rows_kernel(View c, Plan p, const bf16* __restrict__ q, int h_q, Many many,
         if (vs < kSmallScale) unit->z = vs / vc * 0.99999994f, unit->w = 0.f;  // below 1, and the same to 16 bits
       }
       if (now == -2) {
-        put_tail(v_tile, c.tail_v, i, pow2f(14 - tail_e[1]));
+        put_tail(v_tile, c.tail_v, i, pow2f(kTailV - tail_e[1]));
       } else {
 #pragma unroll
         for (int z = 0; z < NP; ++z) {

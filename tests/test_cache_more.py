@@ -233,6 +233,23 @@ def test_converted_keys_of_small_magnitudes(W, power):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,B,hq,n", [(128, 16, 8, 19), (64, 32, 3, 60), (128, 128, 40, 3), (64, 16, 96, 1), (64, 32, 3, 9)])
+def test_small_weights_beside_a_sharp_softmax(kind, d, B, hq, n):
+    """Keys with a millionth of the weight, where the heaviest key's value is near zero in a channel: in whole blocks and
+    in the partial one, for tiles of every size."""
+    for seed in range(4):
+        r = Run(2, 400 // B + 30, 400 // B + 10, hq, 1, d, B, kind, 0, 4, seed=seed, scale=4.0)
+        for held in (B // 2 + 1, 3 * B):
+            plan, want, _ = r.tables([held, 2 * B])
+            assert r.append(plan, want) == 0
+            plan, want, _ = r.tables([n, n + 1])
+            k, v = r.rand(2 * n + 1, 1, d), r.rand(2 * n + 1, 1, d)
+            assert r.append(plan, want, k, v) == 0
+            r.queries(plan, want)
+
+
+@gpu
 @pytest.mark.parametrize("hq,n", [(4, 1), (96, 1), (4, 30)])
 def test_lse_does_not_depend_on_the_values(hq, n):
     """V scales on either side of where the kernels take another path, and of their ends, set in the cache by hand."""
